@@ -28,6 +28,7 @@ __all__ = [
     "gtattn_csr_validate", "gtattn_status_string", "gtattn_profile_enable", "gtattn_profile_read",
     "sparse_mha", "GTATTN_F32", "GTATTN_BF16", "GTATTN_BF16_OUT_F32",
     "GTATTN_KERNEL_AUTO", "GTATTN_KERNEL_VECTOR", "GTATTN_KERNEL_GENERIC", "GTATTN_KERNEL_NARROW",
+    "Cache", "gtattn_cache_slots", "gtattn_cache_append", "gtattn_cache_select", "gtattn_fwd_cache",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -42,8 +43,9 @@ EXPORTED_SYMBOLS = (
     "gtattn_coo_to_csr", "gtattn_csr_validate", "gtattn_profile_enable", "gtattn_profile_read",
     "gtattn_fwd_noalloc", "gtattn_fwd_host", "gtattn_fwd_bias", "gtattn_fwd_weighted", "gtattn_bwd",
     "gtattn_fwd_ndh", "gtattn_fwd_proj", "gtattn_device_errors", "gtattn_bwd_plan", "gtattn_fwd_plan_stats",
+    "gtattn_cache_slots", "gtattn_cache_append", "gtattn_cache_select", "gtattn_fwd_cache",
 )
-KCAT_NAMES = ("bin", "rows", "combine", "softmax", "dense", "gemm")
+KCAT_NAMES = ("bin", "rows", "combine", "softmax", "dense", "gemm", "cache")
 
 
 class GtattnError(RuntimeError):
@@ -77,6 +79,12 @@ class PlanInfo(ctypes.Structure):
 class Profile(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_int32 * 8), ("groups", ctypes.c_int32 * 8),
                 ("ms", ctypes.c_double * 8)]
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k8", ctypes.c_void_p), ("v8", ctypes.c_void_p), ("kscale", ctypes.c_void_p),
+                ("vscale", ctypes.c_void_p), ("kmean", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -117,6 +125,10 @@ def load(path: str | None = None):
             "gtattn_device_errors": ([vp, i32], i32),
             "gtattn_bwd_plan": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, f32, i32, vp], i32),
             "gtattn_fwd_plan_stats": ([vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, f32, i32, vp], i32),
+            "gtattn_cache_slots": ([vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp], i32),
+            "gtattn_cache_append": ([vp, vp, vp, vp, i64, i32, vp], i32),
+            "gtattn_cache_select": ([vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, vp], i32),
+            "gtattn_fwd_cache": ([vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, f32, i32, vp], i32),
             "gtattn_profile_enable": ([i32], i32),
             "gtattn_profile_read": ([vp, i32], i32),
         }
@@ -377,6 +389,156 @@ class Plan:
             self.close()
         except Exception:
             pass
+
+
+# --------------------------------------------------------------------------
+# the 8-bit K/V cache
+# --------------------------------------------------------------------------
+class Cache:
+    """A K/V cache held in 8 bits (``gtattn_cache``): the tensors it is made of.
+
+    k8, v8: e4m3 codes [pages, Hkv, page, D] (torch.float8_e4m3fn or uint8);
+    kscale, vscale: fp32 [pages, Hkv]; kmean: bf16 [pages, Hkv, D] or None.
+    Any of them may be None where no call needs it (k8, or kmean and
+    ``page``, give the sizes).  The tensors stay the caller's: calls write
+    into them, and the object keeps them alive."""
+
+    def __init__(self, k8, v8, kscale, vscale, kmean=None, page=None):
+        import torch
+        if k8 is not None:
+            pages, Hkv, tokens, D = k8.shape
+            if page is not None and int(page) != tokens:
+                raise ValueError(f"page is {page}, the tiles hold {tokens} tokens")
+        elif kmean is not None and page is not None:
+            (pages, Hkv, D), tokens = kmean.shape, int(page)
+        else:
+            raise ValueError("give k8, or kmean and page")
+        codes = (torch.float8_e4m3fn, torch.uint8)
+        dev = None
+        for name, x, shape, dtypes in (("k8", k8, (pages, Hkv, tokens, D), codes),
+                                       ("v8", v8, (pages, Hkv, tokens, D), codes),
+                                       ("kscale", kscale, (pages, Hkv), (torch.float32,)),
+                                       ("vscale", vscale, (pages, Hkv), (torch.float32,)),
+                                       ("kmean", kmean, (pages, Hkv, D), (torch.bfloat16,))):
+            if x is None:
+                continue
+            if tuple(x.shape) != shape or x.dtype not in dtypes:
+                raise ValueError(f"{name}: expected {shape} of {dtypes[0]}, got {tuple(x.shape)} of {x.dtype}")
+            if dev is not None and x.device != dev:
+                raise ValueError(f"{name} is on {x.device}, the cache on {dev}")
+            dev = x.device
+        self.k8, self.v8, self.kscale, self.vscale, self.kmean = k8, v8, kscale, vscale, kmean
+        self.pages, self.Hkv, self.page, self.D = pages, Hkv, tokens, D
+        self.device = dev
+        self._struct = _CacheStruct(_ptr(k8), _ptr(v8), _ptr(kscale), _ptr(vscale), _ptr(kmean), pages, tokens, Hkv, D)
+        self._ref = ctypes.addressof(self._struct)
+        self._dev = dev.index if dev.type == "cuda" else -1
+
+    @classmethod
+    def empty(cls, pages, Hkv, D, page=64, device="cuda", means=True):
+        """A cache of unused pages (``means``: with the page means that
+        gtattn_cache_select reads)."""
+        import torch
+        tile = (int(pages), int(Hkv), int(page), int(D))
+        k8, v8 = (torch.zeros(tile, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = (torch.zeros(tile[:2], dtype=torch.float32, device=device) for _ in range(2))
+        km = torch.zeros(tile[0], tile[1], tile[3], dtype=torch.bfloat16, device=device) if means else None
+        return cls(k8, v8, ks, vs, km)
+
+
+def _arg(x, name, least, dtypes, dev):
+    """Device pointer of a contiguous CUDA tensor on device ``dev`` with at
+    least ``least`` elements of one of ``dtypes`` (ints pass as pointers)."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
+    n = x.numel()
+    if n < least:
+        raise ValueError(f"{name}: expected at least {least} elements, got {n}")
+    if n and x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, the call runs on cuda:{dev}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return x.data_ptr() or None
+
+
+def _call_dev(cache=None):
+    """Current CUDA device, on which the calls run; the cache has to be on it."""
+    import torch
+    dev = torch.cuda.current_device()
+    if cache is not None and cache._dev != dev:
+        raise ValueError(f"the cache is on {cache.device}, the call runs on cuda:{dev}")
+    return dev
+
+
+def _types(dtype):
+    """(input, output) torch dtypes of a gtattn_dtype, as tuples for _arg."""
+    import torch
+    f, b = (torch.float32,), (torch.bfloat16,)
+    if dtype == GTATTN_F32:
+        return f, f
+    if dtype == GTATTN_BF16:
+        return b, b
+    if dtype == GTATTN_BF16_OUT_F32:
+        return b, f
+    raise GtattnError(GTATTN_ERR_INVALID_ARG, "dtype")
+
+
+def _i32():
+    import torch
+    return (torch.int32,)
+
+
+def gtattn_cache_slots(length, add, table, free_pages, new_length, tok_off, slots, counts, S, max_pages, n_free, T, page,
+                       stream=None):
+    """Pages and slots for the tokens that S requests add: takes pages from
+    ``free_pages`` into ``table`` [S, max_pages], writes ``new_length`` [S],
+    ``tok_off`` [S+1], ``slots`` [T] (-1: no place) and ``counts`` [3] (pages
+    taken, rows, requests refused); all int32 CUDA tensors."""
+    dev, i = _call_dev(), _i32()
+    _check(load().gtattn_cache_slots(
+        _arg(length, "length", S, i, dev), _arg(add, "add", S, i, dev), _arg(table, "table", S * max_pages, i, dev),
+        _arg(free_pages, "free_pages", n_free, i, dev), _arg(new_length, "new_length", S, i, dev),
+        _arg(tok_off, "tok_off", S + 1, i, dev), _arg(slots, "slots", T, i, dev), _arg(counts, "counts", 3, i, dev),
+        S, max_pages, n_free, T, page, _stream(stream)), "gtattn_cache_slots")
+
+
+def gtattn_cache_append(cache, K, V, slots, T, dtype, stream=None):
+    """Stores the keys and values [T, Hkv, D] of T tokens in the cache's
+    ``slots`` (int32 [T], as gtattn_cache_slots lists them), in 8 bits."""
+    dev = _call_dev(cache)
+    t, n = _types(dtype)[0], T * cache.Hkv * cache.D
+    _check(load().gtattn_cache_append(cache._ref, _arg(K, "K", n, t, dev), _arg(V, "V", n, t, dev),
+                                      _arg(slots, "slots", T, _i32(), dev), T, dtype, _stream(stream)),
+           "gtattn_cache_append")
+
+
+def gtattn_cache_select(cache, Q, table, length, tok_off, sel, S, T, max_pages, H, n_sel, dtype, stream=None):
+    """The pages each row and K/V head reads: its own and the n_sel - 1
+    earlier ones whose mean key scores highest; ``sel`` [T, Hkv, n_sel]
+    int32, ascending, -1 where there are fewer."""
+    dev, i = _call_dev(cache), _i32()
+    _check(load().gtattn_cache_select(
+        cache._ref, _arg(Q, "Q", T * H * cache.D, _types(dtype)[0], dev), _arg(table, "table", S * max_pages, i, dev),
+        _arg(length, "length", S, i, dev), _arg(tok_off, "tok_off", S + 1, i, dev),
+        _arg(sel, "sel", T * cache.Hkv * n_sel, i, dev), S, T, max_pages, H, n_sel, dtype, _stream(stream)),
+        "gtattn_cache_select")
+
+
+def gtattn_fwd_cache(cache, Q, table, length, tok_off, out, S, T, max_pages, H, scale, dtype, sel=None, n_sel=0,
+                     stream=None):
+    """Attention of T new rows Q [T, H, D] over the cache: all tokens of
+    their request up to each row's position, or those in the pages ``sel``
+    ([T, Hkv, n_sel] int32) names."""
+    dev, i = _call_dev(cache), _i32()
+    ti, to = _types(dtype)
+    n = T * H * cache.D
+    _check(load().gtattn_fwd_cache(
+        cache._ref, _arg(Q, "Q", n, ti, dev), _arg(table, "table", S * max_pages, i, dev),
+        _arg(length, "length", S, i, dev), _arg(tok_off, "tok_off", S + 1, i, dev),
+        _arg(sel, "sel", T * cache.Hkv * n_sel, i, dev), _arg(out, "out", n, to, dev), S, T, max_pages, H, n_sel, scale,
+        dtype, _stream(stream)), "gtattn_fwd_cache")
 
 
 def sparse_mha(indptr, indices, Q, K, V, scale=None, out=None, plan=None, stream=None):

@@ -1,0 +1,72 @@
+// cache.cuh -- internal definitions of the 8-bit K/V cache operators
+// (cache.cu: slots and append; cache_select.cu: page selection;
+// cache_attn.cu: attention over the cache).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace gt {
+
+constexpr int kCacheMaxD = 256;
+constexpr int kCacheMaxHeads = 1024;
+// scale exponents: an all-zero page gets 2^-64; fp32's largest value needs 2^120
+constexpr int kScaleMinExp = -64, kScaleMaxExp = 120;
+
+// Device view of a gtattn_cache.
+struct CacheView {
+    uint8_t* k8;
+    uint8_t* v8;
+    float* kscale;
+    float* vscale;
+    __nv_bfloat16* kmean;
+    int pages, page, lp;   // page = 1 << lp
+    int Hkv, D;
+};
+
+// The requests' side of a call: new token rows [tok_off[s], tok_off[s+1]) of
+// request s are its last ones, at positions length[s] - n .. length[s] - 1.
+struct CacheRows {
+    const int* table;     // [S, max_pages] page ids
+    const int* length;    // [S]
+    const int* tok_off;   // [S + 1]
+    int S, T, max_pages;
+};
+
+// Host checks shared by the entry points; `need` is a mask of what the call
+// reads of the cache: 1 k8/v8 and their scales, 2 kmean.
+gtattn_status check_cache(const gtattn_cache* c, int need, CacheView* v);
+gtattn_status check_cache_rows(const int32_t* table, const int32_t* length, const int32_t* tok_off, int64_t S,
+                               int64_t T, int64_t max_pages, int page, CacheRows* r);
+
+// Request of token row t (t < tok_off[S]): the largest s with tok_off[s] <= t.
+__device__ __forceinline__ int request_of(const int* __restrict__ tok_off, int S, int t) {
+    int lo = 0, hi = S;   // tok_off[lo] <= t < tok_off[hi]
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (__ldg(tok_off + m) <= t) lo = m;
+        else hi = m;
+    }
+    return lo;
+}
+
+// Position of row t of request s in its request; -1 when the request holds
+// fewer tokens than it has rows, capped at the table's last position.
+__device__ __forceinline__ int position_of(const CacheRows& r, int page, int s, int t) {
+    const long long p = static_cast<long long>(__ldg(r.length + s)) - (__ldg(r.tok_off + s + 1) - t);
+    const long long last = static_cast<long long>(r.max_pages) * page - 1;
+    return static_cast<int>(p < -1 ? -1 : p > last ? last : p);
+}
+
+__device__ __forceinline__ float e4m3_f32(uint8_t x) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(x, __NV_E4M3)));
+}
+// Nearest e4m3 value, ties to even, saturating; NaN and infinities give NaN.
+__device__ __forceinline__ uint8_t f32_e4m3(float x) {
+    if (!(fabsf(x) < INFINITY)) return 0x7f;
+    return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+}  // namespace gt

@@ -1,0 +1,140 @@
+// cache_attn.cu -- attention of new tokens over the 8-bit cache: all pages up
+// to the token's position, or the pages selected for it.
+#include "cache.cuh"
+
+#include <algorithm>
+
+namespace gt {
+namespace {
+
+struct CacheAttn {
+    CacheView c;
+    CacheRows r;
+    const void* Q;
+    void* out;
+    const int* sel;   // [T, Hkv, n_sel] page numbers within the request, or null
+    int H, G, n_sel;
+    float qscale;     // scale * log2(e)
+};
+
+constexpr int kGenWarps = 4;
+constexpr int kGenVpl = kCacheMaxD / 32;
+
+// Any head width: a block per (token, query head), its warps over the pages,
+// lanes over the features; one pass with the running maximum and sum.
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(kGenWarps * 32) k_cache_attn_generic(CacheAttn a, int64_t n_items) {
+    __shared__ float sm_acc[kGenWarps][kCacheMaxD];
+    __shared__ float sm_m[kGenWarps], sm_l[kGenWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const CacheView& c = a.c;
+    const int end = a.r.tok_off[a.r.S];
+    const int D = c.D;
+    for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
+        const int t = (int)(it / a.H), h = (int)(it % a.H), g = h / a.G;
+        if (t >= end) return;
+        const int s = request_of(a.r.tok_off, a.r.S, t);
+        const int pos = position_of(a.r, c.page, s, t);
+        float q[kGenVpl], acc[kGenVpl];
+#pragma unroll
+        for (int k = 0; k < kGenVpl; ++k) {
+            const int d = lane + 32 * k;
+            q[k] = d < D ? load_elem(static_cast<const TI*>(a.Q), it * D + d) : 0.f;
+            acc[k] = 0.f;
+        }
+        float m = -INFINITY, l = 0.f;
+        const int n_pages = pos < 0 ? 0 : a.sel ? a.n_sel : (pos >> c.lp) + 1;
+        for (int i = warp; i < n_pages; i += kGenWarps) {
+            const int p = a.sel ? a.sel[((int64_t)t * c.Hkv + g) * a.n_sel + i] : i;
+            if (p < 0 || p > (pos >> c.lp)) continue;
+            const int pid = a.r.table[(int64_t)s * a.r.max_pages + p];
+            if ((unsigned)pid >= (unsigned)c.pages) continue;
+            const int64_t ph = (int64_t)pid * c.Hkv + g;
+            const float ks = c.kscale[ph] * a.qscale, vs = c.vscale[ph];
+            const uint8_t* kt = c.k8 + ph * c.page * D;
+            const uint8_t* vt = c.v8 + ph * c.page * D;
+            const int n = min(c.page, pos - p * c.page + 1);
+            for (int j = 0; j < n; ++j) {
+                float x = 0.f;
+#pragma unroll
+                for (int k = 0; k < kGenVpl; ++k) {
+                    const int d = lane + 32 * k;
+                    if (d < D) x += q[k] * e4m3_f32(kt[j * D + d]);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                x *= ks;
+                const float mn = fmaxf(m, x);
+                const float mu = mn == -INFINITY ? 0.f : mn;
+                const float w = ex2(x - mu), cr = ex2(m - mu);
+                l = l * cr + w;
+                m = mn;
+#pragma unroll
+                for (int k = 0; k < kGenVpl; ++k) {
+                    const int d = lane + 32 * k;
+                    if (d < D) acc[k] = acc[k] * cr + w * (vs * e4m3_f32(vt[j * D + d]));
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kGenVpl; ++k) sm_acc[warp][lane + 32 * k] = acc[k];
+        if (lane == 0) { sm_m[warp] = m; sm_l[warp] = l; }
+        __syncthreads();
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kGenWarps; ++w) mm = fmaxf(mm, sm_m[w]);
+        if (mm == -INFINITY) mm = 0.f;
+        float total = 0.f;
+#pragma unroll
+        for (int w = 0; w < kGenWarps; ++w) total += sm_l[w] * ex2(sm_m[w] - mm);
+        for (int d = threadIdx.x; d < D; d += kGenWarps * 32) {
+            float o = 0.f;
+#pragma unroll
+            for (int w = 0; w < kGenWarps; ++w) o += sm_acc[w][d] * ex2(sm_m[w] - mm);
+            store_elem(static_cast<TO*>(a.out), it * D + d, total == 0.f ? 0.f : o / total);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+}  // namespace gt
+
+using namespace gt;
+
+extern "C" gtattn_status gtattn_fwd_cache(const gtattn_cache* cache, const void* Q, const int32_t* table,
+                                          const int32_t* length, const int32_t* tok_off, const int32_t* sel, void* out,
+                                          int64_t S, int64_t T, int64_t max_pages, int H, int n_sel, float scale,
+                                          gtattn_dtype dtype, cudaStream_t stream) {
+    CacheAttn a{};
+    GT_TRY(check_cache(cache, 1, &a.c));
+    GT_TRY(check_cache_rows(table, length, tok_off, S, T, max_pages, a.c.page, &a.r));
+    if (dtype != GTATTN_F32 && dtype != GTATTN_BF16 && dtype != GTATTN_BF16_OUT_F32) return GTATTN_ERR_INVALID_ARG;
+    if (H < 1 || H > kCacheMaxHeads || H % a.c.Hkv) return GTATTN_ERR_INVALID_ARG;
+    if (sel ? (n_sel < 1 || n_sel > (1 << 20)) : n_sel != 0) return GTATTN_ERR_INVALID_ARG;
+    if (T > 0 && (!Q || !out)) return GTATTN_ERR_INVALID_ARG;
+    const uintptr_t esz = dtype == GTATTN_F32 ? 4 : 2, osz = dtype == GTATTN_BF16 ? 2 : 4;
+    if ((reinterpret_cast<uintptr_t>(Q) & (esz - 1)) || (reinterpret_cast<uintptr_t>(out) & (osz - 1)) ||
+        (reinterpret_cast<uintptr_t>(sel) & 3u))
+        return GTATTN_ERR_INVALID_ARG;
+    if (T * H >= (1ll << 31)) return GTATTN_ERR_UNSUPPORTED;
+    if (T == 0 || S == 0) return GTATTN_OK;
+    a.Q = Q;
+    a.out = out;
+    a.sel = sel;
+    a.H = H;
+    a.G = H / a.c.Hkv;
+    a.n_sel = n_sel;
+    a.qscale = scale * kLog2e;
+    const int64_t items = T * H;
+    const int blocks = (int)std::min<int64_t>(items, num_sms() * 16);
+    ProfScope ps(GTATTN_KCAT_CACHE, 1, stream);
+    if (dtype == GTATTN_F32)
+        k_cache_attn_generic<float, float><<<blocks, kGenWarps * 32, 0, stream>>>(a, items);
+    else if (dtype == GTATTN_BF16)
+        k_cache_attn_generic<__nv_bfloat16, __nv_bfloat16><<<blocks, kGenWarps * 32, 0, stream>>>(a, items);
+    else
+        k_cache_attn_generic<__nv_bfloat16, float><<<blocks, kGenWarps * 32, 0, stream>>>(a, items);
+    GT_CUDA(cudaGetLastError());
+    return GTATTN_OK;
+}

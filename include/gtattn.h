@@ -451,6 +451,133 @@ gtattn_status gtattn_csr_validate(const int32_t* indptr, const int32_t* indices,
                                   int64_t nnz, cudaStream_t stream);
 
 /*
+ * The 8-bit K/V cache: keys and values of nodes (tokens) that stay, for new
+ * ones that attend over them -- a batch of requests, each a sequence or graph
+ * that grows node by node.  It is the same softmax(Q K^T / sqrt(d)) V, with
+ * rows that are only the new nodes and columns read from the cache (a store
+ * of this library's design; the source pages have no counterpart).
+ *
+ * The cache is caller-owned device memory cut into `pages` pages of `page`
+ * tokens.  A request holds its tokens in order in the pages its row of a page
+ * table names: table int32 [S, max_pages], token i of request s in page
+ * table[s, i / page] at place i % page.  Per page and K/V head:
+ *   k8, v8:  e4m3 codes [pages, Hkv, page, D]; the value is code * scale.
+ *   kscale, vscale: fp32 [pages, Hkv], powers of two, so that a page whose
+ *            scale grows is rescaled without rounding (but for codes that
+ *            become subnormal).
+ *   kmean:   bf16 [pages, Hkv, D], the mean of the page's stored keys (as
+ *            stored, rounded once): what gtattn_cache_select scores.  May be
+ *            NULL where no call selects.
+ * k8, v8 and kmean are 16-byte aligned, the scales 4-byte.  page is 16, 32 or
+ * 64; 1 <= D <= 256, 1 <= Hkv <= 1024; pages * page < 2^31.  Fields a call
+ * does not use may be NULL (append: kmean; select: all but kmean; attention:
+ * kmean).  The struct is read during the call and not kept.
+ *
+ * Rows: T new tokens stand one request after another; request s has rows
+ * [tok_off[s], tok_off[s+1]) (int32 [S+1], tok_off[0] = 0, non-decreasing,
+ * tok_off[S] <= T), which are its last tokens: with length[s] (int32 [S]) the
+ * tokens it holds, them included, row tok_off[s+1] - 1 is at position
+ * length[s] - 1.  Rows from tok_off[S] on (a padded batch) are not read, and
+ * their results are left as they were.  Page ids outside [0, pages) hold
+ * nothing: attention skips them and their score is 0; a length beyond the
+ * table counts as the table's end.  The contents of tok_off are not checked.
+ * S, T < 2^31 - 1, max_pages * page < 2^31.  Q and out are [T, H, D], H a
+ * multiple of Hkv and at most 1024: query head h reads K/V head h / (H / Hkv).
+ * All calls are asynchronous on `stream`; temporaries come from the
+ * stream-ordered pool.  Results do not change from run to run.
+ */
+typedef struct {
+    void* k8;
+    void* v8;
+    float* kscale;
+    float* vscale;
+    void* kmean;
+    int32_t pages, page, Hkv, D;
+} gtattn_cache;
+
+/*
+ * gtattn_cache_slots -- places for the tokens a batch adds, from the
+ * requests' lengths: takes pages from a free list and lists every new token's
+ * slot (page id * page + place in the page).
+ *   length, add: int32 [S], tokens held and tokens to add.
+ *   table:      [S, max_pages]; entries of newly taken pages are written, the
+ *               others are read only.
+ *   free_pages: int32 [n_free]; taken from the front, in request order.
+ *   new_length: int32 [S], length + add (must not overlap length).
+ *   tok_off:    int32 [S+1], the rows of each request (see above).
+ *   slots:      int32 [T], rows in order; -1 from tok_off[S] on.
+ *   counts:     int32 [3]: pages taken, rows (tok_off[S]), requests refused.
+ * A request is refused -- its new_length stays length, its slots are -1, it
+ * takes no pages -- when length or add is negative or the sum exceeds
+ * max_pages * page (it then has no rows), when the free list ends before its
+ * new pages (those of all requests before it counted), or when its rows would
+ * pass T (tok_off is capped at T).  The others are served.
+ * Errors: INVALID_ARG (null pointers, sizes, alignment), CUDA.
+ */
+gtattn_status gtattn_cache_slots(const int32_t* length, const int32_t* add, int32_t* table,
+                                 const int32_t* free_pages, int32_t* new_length, int32_t* tok_off, int32_t* slots,
+                                 int32_t* counts, int64_t S, int64_t max_pages, int64_t n_free, int64_t T, int page,
+                                 cudaStream_t stream);
+
+/*
+ * gtattn_cache_append -- stores keys and values of T tokens in the cache.
+ *   K, V:  [T, Hkv, D] in the input type of `dtype`.
+ *   slots: int32 [T] as gtattn_cache_slots lists them: a page's new tokens
+ *          stand together, in consecutive slots.  Slots outside
+ *          [0, pages * page) are skipped.  A list that names one page in two
+ *          places, or a slot twice, leaves that page undefined (and touches
+ *          nothing else).
+ * Per page and head: the places before the first new token hold the page's
+ * earlier tokens, those behind the last one hold nothing any more (a request
+ * that was cut back is written over).  With amax the largest |x| of the new
+ * tokens (finite ones), e the least integer with amax <= 448 * 2^e (within
+ * [-64, 120]), the scale becomes max(2^e, the old one if the page has earlier
+ * tokens); earlier codes become e4m3(code * old / new), new ones
+ * e4m3(x / scale), to nearest, ties to even; NaN and infinities become NaN.
+ * kmean, if not NULL, becomes the mean of the page's stored keys.
+ * Errors: INVALID_ARG, CUDA.
+ */
+gtattn_status gtattn_cache_append(const gtattn_cache* cache, const void* K, const void* V, const int32_t* slots,
+                                  int64_t T, gtattn_dtype dtype, cudaStream_t stream);
+
+/*
+ * gtattn_cache_select -- for each row and K/V head the n_sel pages it reads:
+ * the page of its own position, and of the pages before that one the
+ * n_sel - 1 with the highest
+ *   score(p, g) = sum over heads h of group g of <Q[t, h, :], kmean[p, g, :]>
+ * (equal scores: the earlier page; a NaN score counts as the lowest).  The
+ * choice is that of scores in 64 bits, whatever fp32 would make of them.
+ *   Q:   [T, H, D] in the input type of `dtype`.
+ *   sel: int32 [T, Hkv, n_sel], page numbers within the request
+ *        (0 .. position / page), ascending, then -1 where there are fewer.
+ * 1 <= n_sel <= 2^20.  Errors: INVALID_ARG, UNSUPPORTED (T * Hkv >= 2^31),
+ * NO_MEMORY, CUDA.
+ */
+gtattn_status gtattn_cache_select(const gtattn_cache* cache, const void* Q, const int32_t* table,
+                                  const int32_t* length, const int32_t* tok_off, int32_t* sel, int64_t S, int64_t T,
+                                  int64_t max_pages, int H, int n_sel, gtattn_dtype dtype, cudaStream_t stream);
+
+/*
+ * gtattn_fwd_cache -- attention of the new rows over the cache:
+ *   out[t, h, :] = sum_j p_j v_j,  p = softmax_j(scale * q . k_j)
+ * over the tokens j of row t's request up to its own position, or, with
+ * `sel`, over those of them in the pages listed for (t, head group).
+ *   Q:   [T, H, D] in the input type of `dtype`; out: [T, H, D] in its output
+ *        type (must not overlap Q).
+ *   sel: NULL (and n_sel 0), or int32 [T, Hkv, n_sel] as gtattn_cache_select
+ *        writes it, in any order; entries below 0 or past the row's own page
+ *        are skipped, a page listed twice weighs twice.
+ * A row without tokens to read gives zeros.  Accumulation is fp32 and every
+ * row's result reads only the tokens it may see (a NaN in a later token or
+ * an unused place reaches no earlier row).
+ * Errors: INVALID_ARG, UNSUPPORTED (T * H >= 2^31), NO_MEMORY, CUDA.
+ */
+gtattn_status gtattn_fwd_cache(const gtattn_cache* cache, const void* Q, const int32_t* table, const int32_t* length,
+                               const int32_t* tok_off, const int32_t* sel, void* out, int64_t S, int64_t T,
+                               int64_t max_pages, int H, int n_sel, float scale, gtattn_dtype dtype,
+                               cudaStream_t stream);
+
+/*
  * Benchmark instrumentation (not part of the pages' operation).  While
  * enabled, the library brackets each of its kernel launches (or a launch
  * group, for binning) with a pair of CUDA events on the launching stream and
@@ -466,6 +593,7 @@ typedef enum {
     GTATTN_KCAT_SOFTMAX = 3,  /* unfused edge softmax */
     GTATTN_KCAT_DENSE = 4,    /* dense-block tensor-core kernel */
     GTATTN_KCAT_GEMM = 5,     /* projections around the attention (and their weight permutations) */
+    GTATTN_KCAT_CACHE = 6,    /* the 8-bit cache's calls (gtattn_cache_*, gtattn_fwd_cache) */
     GTATTN_KCAT_COUNT = 8
 } gtattn_kernel_category;
 
