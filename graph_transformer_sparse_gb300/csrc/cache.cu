@@ -79,35 +79,128 @@ __device__ __forceinline__ void slots_need(const SlotsArgs& a, int s, int& len, 
     need = bad ? 0 : static_cast<int>((static_cast<unsigned>(len + add) + up) / a.page) - have;
 }
 
-// Simplest form: one thread walks the requests in order.
-__global__ void k_slots_serial(SlotsArgs a) {
-    if (threadIdx.x || blockIdx.x) return;
-    long long tok = 0, pages = 0;
-    int taken = 0, refused = 0;
-    for (int s = 0; s < a.S; ++s) {
-        int len, add, have, need, bad;
-        slots_need(a, s, len, add, have, need, bad);
-        const bool ok = !bad && (add == 0 || tok + add <= a.T) && (need == 0 || pages + need <= a.n_free);
-        a.tok_off[s] = (int)min(tok, (long long)a.T);
-        a.new_len[s] = ok ? len + add : len;
-        refused += !ok;
-        if (ok) {
-            if (need) taken = (int)(pages + need);
-            for (int p = 0; p < need; ++p) a.table[(int64_t)s * a.max_pages + have + p] = a.free_pages[pages + p];
-        }
-        for (int i = 0; i < add && tok + i < a.T; ++i) {
-            const int pos = len + i;
-            a.slots[tok + i] = ok ? a.table[(int64_t)s * a.max_pages + pos / a.page] * a.page + pos % a.page : -1;
-        }
+// A block owns kSlotThreads consecutive requests: it adds up the sizes of all
+// requests before them, scans its own, and its threads then take the
+// requests' tokens one by one (a binary search in shared memory names the
+// token's request), so that one long prompt is spread as evenly as many short
+// ones; gridDim.y blocks share a group's tokens.  Bound by latency: two
+// dependent loads, two scans and the stores.
+constexpr int kSlotThreads = 256;
+
+// exclusive scan over the block; *total receives the sum
+__device__ __forceinline__ long long slot_scan(long long v, long long* total) {
+    __shared__ long long sums[kSlotThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSlotThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+    }
+    *total = all;
+    return before + x - v;
+}
+
+__global__ void __launch_bounds__(kSlotThreads) k_slots(SlotsArgs a, int lp) {
+    __shared__ long long s_tok[kSlotThreads + 1];                  // first token of each own request
+    __shared__ int s_len[kSlotThreads], s_have[kSlotThreads], s_page[kSlotThreads];   // s_page: first new page; -1: refused
+    const int tid = threadIdx.x, s0 = blockIdx.x * kSlotThreads, s = s0 + tid;
+    const bool lead = blockIdx.y == 0, final_block = blockIdx.x == gridDim.x - 1;
+    int len = 0, add = 0, have = 0, need = 0, bad = 0;
+    // everything before this block's requests
+    long long tok = 0, pages = 0, refused = 0;
+    for (int i = tid; i < s0; i += kSlotThreads) {
+        slots_need(a, i, len, add, have, need, bad);
         tok += add;
         pages += need;
+        refused += bad;
     }
-    const int end = (int)min(tok, (long long)a.T);
-    a.tok_off[a.S] = end;
-    for (int t = end; t < a.T; ++t) a.slots[t] = -1;
-    a.counts[0] = taken;
-    a.counts[1] = end;
-    a.counts[2] = refused;
+    len = add = have = need = bad = 0;
+    if (s < a.S) slots_need(a, s, len, add, have, need, bad);
+    long long tok0 = 0, pages0 = 0, own_tok, own_pages;
+    if (s0 > 0) {
+        slot_scan(tok, &tok0);
+        slot_scan(pages, &pages0);
+    }
+    const long long t_at = tok0 + slot_scan(add, &own_tok), p_at = pages0 + slot_scan(need, &own_pages);
+    const bool ok = !bad && (add == 0 || t_at + add <= a.T) && (need == 0 || p_at + need <= a.n_free);
+    s_tok[tid] = t_at;
+    s_len[tid] = len;
+    s_have[tid] = have;
+    s_page[tid] = ok ? static_cast<int>(p_at) : -1;
+    if (lead && s < a.S) {
+        a.tok_off[s] = static_cast<int>(min(t_at, (long long)a.T));
+        a.new_len[s] = ok ? len + add : len;
+    }
+    __syncthreads();
+    const long long end = min(tok0 + own_tok, (long long)a.T);
+    const int mask = a.page - 1;
+    for (long long t = tok0 + blockIdx.y * kSlotThreads + tid; t < end; t += static_cast<long long>(gridDim.y) * kSlotThreads) {
+        int lo = 0;      // the last own request that begins at or before t
+#pragma unroll
+        for (int step = kSlotThreads / 2; step > 0; step >>= 1)
+            if (s_tok[lo + step] <= t) lo += step;
+        int slot = -1;
+        if (s_page[lo] >= 0) {
+            const int pos = s_len[lo] + static_cast<int>(t - s_tok[lo]), p = pos >> lp;
+            int* row = a.table + static_cast<int64_t>(s0 + lo) * a.max_pages;
+            int id;
+            if (p >= s_have[lo]) {     // a new page: its first token is a new one, and writes it down
+                id = a.free_pages[s_page[lo] + p - s_have[lo]];
+                if ((pos & mask) == 0) row[p] = id;
+            } else {
+                id = row[p];
+            }
+            slot = static_cast<int>(static_cast<unsigned>(id) * a.page + (pos & mask));
+        }
+        a.slots[t] = slot;
+    }
+    if (!final_block) return;
+    for (long long t = end + blockIdx.y * kSlotThreads + tid; t < a.T; t += static_cast<long long>(gridDim.y) * kSlotThreads)
+        a.slots[t] = -1;
+    if (!lead) return;
+    long long taken = pages0 + own_pages, no = 0;
+    if (tok0 + own_tok <= a.T && pages0 + own_pages <= a.n_free) {     // all fit: only bad sizes are refused
+        slot_scan(refused + bad, &no);
+    } else {                                                           // walk them all again
+        long long carry_t = 0, carry_p = 0;
+        long long best = 0;
+        refused = 0;
+        for (int i0 = 0; i0 < a.S; i0 += kSlotThreads) {
+            len = add = have = need = bad = 0;
+            if (i0 + tid < a.S) slots_need(a, i0 + tid, len, add, have, need, bad);
+            long long all_t, all_p;
+            const long long ta = carry_t + slot_scan(add, &all_t), pa = carry_p + slot_scan(need, &all_p);
+            const bool fine = !bad && (add == 0 || ta + add <= a.T) && (need == 0 || pa + need <= a.n_free);
+            if (i0 + tid < a.S) refused += !fine;
+            if (fine && need) best = pa + need;      // (rises with the request)
+            carry_t += all_t;
+            carry_p += all_p;
+        }
+        slot_scan(refused, &no);
+        // the largest of the threads' last pages
+        __shared__ long long s_best[kSlotThreads];
+        s_best[tid] = best;
+        __syncthreads();
+        taken = 0;
+        for (int i = 0; i < kSlotThreads; ++i) taken = max(taken, s_best[i]);
+    }
+    if (tid == 0) {
+        const int all = static_cast<int>(min(tok0 + own_tok, (long long)a.T));
+        a.tok_off[a.S] = all;
+        a.counts[0] = static_cast<int>(taken);
+        a.counts[1] = all;
+        a.counts[2] = static_cast<int>(no);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -139,7 +232,7 @@ k_append(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const in
     if (f > 0 && t > 0 && slots[t - 1] == slot - 1) return;
     if (tid == 0) {
         int n = 1;
-        while (f + n < c.page && t + n < T_rows && slots[t + n] == slot + n) ++n;
+        while (f + n < c.page && T_rows - t > n && slots[t + n] == slot + n) ++n;
         s_n = n;
     }
     __syncthreads();
@@ -179,6 +272,152 @@ k_append(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const in
     }
 }
 
+
+// The same for D a power of two from 8 on, rows 16-byte aligned: a thread
+// takes 8 features at a time, always the same 8 columns, so the column sums
+// of the mean stay in its registers (they are exact in fp32, in any order).
+// A block looks at `span` consecutive tokens and takes the runs that begin
+// there: one token in a small batch (a run per block), 32 in a large one,
+// where most tokens begin no run.
+// Bound by memory: the new rows are read once from DRAM (the second pass over
+// them hits L1), a page's earlier keys are read for its mean.
+__device__ __forceinline__ uint2 eight_e4m3(const float (&x)[8]) {
+    uint32_t h[4];
+    float worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+        worst = fmaxf(worst, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    }
+    if (worst == INFINITY) {     // (a NaN converts to NaN by itself)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = f32_e4m3(x[2 * i]) | (f32_e4m3(x[2 * i + 1]) << 8);
+    }
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+__device__ __forceinline__ void eight_f32(uint2 c, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = (i < 2 ? c.x : c.y) >> (16 * (i & 1));
+        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3)));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads)
+k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const int* __restrict__ slots, int T_rows,
+          int span, int l8) {       // l8 = log2(D / 8)
+    __shared__ float red[kAppendThreads / 32];
+    __shared__ float cols[kCacheMaxD];
+    const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    const bool is_v = blockIdx.z != 0;
+    const int D = c.D, HD = c.Hkv * D, W = 1 << l8;
+    const unsigned total = static_cast<unsigned>(c.pages) * c.page;
+    const int first = static_cast<int>(min(static_cast<long long>(blockIdx.x) * span, 0x7fffffffll));
+    const int cc = tid & (W - 1), rr = tid >> l8, rows = kAppendThreads >> l8;   // this thread's columns, first row, row step
+    // every warp finds the block's runs: lane i looks at token first + i
+    bool begins = false;
+    if (lane < span && T_rows - first > lane) {
+        const int slot = slots[first + lane];
+        begins = static_cast<unsigned>(slot) < total &&
+                 ((slot & (c.page - 1)) == 0 || first + lane == 0 || slots[first + lane - 1] != slot - 1);
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, begins);
+    while (todo) {
+        const int t = first + __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int slot = slots[t];
+        const int f = slot & (c.page - 1), pid = slot >> c.lp;
+        // run length: tokens t + i in slot + i, as far as the page goes
+        int n;
+        {
+            const int i0 = lane, i1 = lane + 32;
+            const bool b0 = !(f + i0 < c.page && T_rows - t > i0 && slots[t + i0] == slot + i0);
+            const bool b1 = !(f + i1 < c.page && T_rows - t > i1 && slots[t + i1] == slot + i1);
+            const unsigned m0 = __ballot_sync(0xffffffffu, b0), m1 = __ballot_sync(0xffffffffu, b1);
+            n = m0 ? __ffs(m0) - 1 : m1 ? 32 + __ffs(m1) - 1 : 64;
+        }
+        const T* x = (is_v ? V : K) + static_cast<int64_t>(t) * HD + g * D + cc * 8;
+        const int64_t ph = static_cast<int64_t>(pid) * c.Hkv + g;
+        float* sp = (is_v ? c.vscale : c.kscale) + ph;
+        uint8_t* tile = (is_v ? c.v8 : c.k8) + (ph << c.lp) * D + cc * 8;
+        const float old = f > 0 ? *sp : 0.f;
+        float amax = 0.f;
+#pragma unroll 4
+        for (int i = rr; i < n; i += rows) {
+            Eight<T> e;
+            e.load(x + static_cast<int64_t>(i) * HD);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float v = fabsf(e.x[k]);
+                if (v < INFINITY) amax = fmaxf(amax, v);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        __syncthreads();                                    // (red and cols of the run before are read)
+        if (lane == 0) red[tid >> 5] = amax;
+        const bool mean = !is_v && c.kmean;
+        if (mean)
+            for (int d = tid; d < D; d += kAppendThreads) cols[d] = 0.f;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
+        const float now = fmaxf(old, power_scale(amax));
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const bool grown = f > 0 && now != old;
+        if (grown || mean) {
+            const float ratio = grown ? old / now : 1.f;
+#pragma unroll 4
+            for (int i = rr; i < f; i += rows) {
+                uint2* p = reinterpret_cast<uint2*>(tile + i * D);
+                uint2 code = *p;
+                float y[8];
+                eight_f32(code, y);
+                if (grown) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] *= ratio;
+                    code = eight_e4m3(y);
+                    *p = code;
+                    eight_f32(code, y);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] += y[k];
+            }
+        }
+        const float inv = 1.f / now;                        // (a power of two: exact)
+#pragma unroll 4
+        for (int i = rr; i < n; i += rows) {
+            Eight<T> e;
+            e.load(x + static_cast<int64_t>(i) * HD);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) e.x[k] *= inv;
+            const uint2 code = eight_e4m3(e.x);
+            *reinterpret_cast<uint2*>(tile + (f + i) * D) = code;
+            if (mean) {
+                float y[8];
+                eight_f32(code, y);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] += y[k];
+            }
+        }
+        if (tid == 0) *sp = now;                            // (everyone has read `old`: two barriers ago)
+        if (mean) {
+            // (exact sums: the order of the additions does not matter)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                for (int o = W; o < 32; o <<= 1) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+                if (lane < W) atomicAdd(&cols[cc * 8 + k], sum[k]);
+            }
+            __syncthreads();
+            for (int d = tid; d < D; d += kAppendThreads)
+                c.kmean[ph * D + d] = __float2bfloat16_rn(cols[d] * now / static_cast<float>(f + n));
+        }
+    }
+}
+
 }  // namespace
 }  // namespace gt
 
@@ -203,7 +442,10 @@ extern "C" gtattn_status gtattn_cache_slots(const int32_t* length, const int32_t
     const SlotsArgs a{length, add, table, free_pages, new_length, tok_off, slots, counts,
                       (int)S, (int)max_pages, (int)n_free, (int)T, page};
     ProfScope ps(GTATTN_KCAT_CACHE, 1, stream);
-    k_slots_serial<<<1, 32, 0, stream>>>(a);
+    const int groups = std::max<int>(1, (int)((S + kSlotThreads - 1) / kSlotThreads));
+    // blocks of a group: about 1024 tokens each, all groups within a wave or two
+    const int share = (int)std::min<int64_t>(std::max<int64_t>(1, T / groups / 1024), std::max(1, 4 * num_sms() / groups));
+    k_slots<<<dim3(groups, share), kSlotThreads, 0, stream>>>(a, page == 16 ? 4 : page == 32 ? 5 : 6);
     GT_CUDA(cudaGetLastError());
     return GTATTN_OK;
 }
@@ -222,6 +464,23 @@ extern "C" gtattn_status gtattn_cache_append(const gtattn_cache* cache, const vo
         return GTATTN_ERR_INVALID_ARG;
     if (T == 0 || c.pages == 0) return GTATTN_OK;
     ProfScope ps(GTATTN_KCAT_CACHE, 1, stream);
+    const bool eights = c.D >= 8 && (c.D & (c.D - 1)) == 0 &&
+                        ((reinterpret_cast<uintptr_t>(K) | reinterpret_cast<uintptr_t>(V)) & 15u) == 0;
+    if (eights) {
+        int l8 = 0;
+        while ((8 << l8) < c.D) ++l8;
+        const int64_t per_sm16 = T * c.Hkv * 2 / (16 * num_sms());
+        const int span = (int)std::min<int64_t>(32, std::max<int64_t>(1, per_sm16));
+        const dim3 grid((unsigned)((T + span - 1) / span), c.Hkv, 2);
+        if (dtype == GTATTN_F32)
+            k_append8<float><<<grid, kAppendThreads, 0, stream>>>(c, static_cast<const float*>(K),
+                                                                   static_cast<const float*>(V), slots, (int)T, span, l8);
+        else
+            k_append8<__nv_bfloat16><<<grid, kAppendThreads, 0, stream>>>(
+                c, static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), slots, (int)T, span, l8);
+        GT_CUDA(cudaGetLastError());
+        return GTATTN_OK;
+    }
     const dim3 grid((unsigned)T, c.Hkv, 2);
     if (dtype == GTATTN_F32)
         k_append<float><<<grid, kAppendThreads, 0, stream>>>(c, static_cast<const float*>(K),

@@ -69,4 +69,23 @@ __device__ __forceinline__ uint8_t f32_e4m3(float x) {
     return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
+// Eight features by 16-byte loads (16-byte aligned).
+template <typename T> struct Eight;
+template <> struct Eight<float> {
+    float x[8];
+    __device__ __forceinline__ void load(const float* p) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+template <> struct Eight<__nv_bfloat16> {
+    float x[8];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p);
+        x[0] = bf16lo(a.x); x[1] = bf16hi(a.x); x[2] = bf16lo(a.y); x[3] = bf16hi(a.y);
+        x[4] = bf16lo(a.z); x[5] = bf16hi(a.z); x[6] = bf16lo(a.w); x[7] = bf16hi(a.w);
+    }
+};
+
 }  // namespace gt

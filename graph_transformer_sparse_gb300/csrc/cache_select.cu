@@ -1,5 +1,19 @@
 // cache_select.cu -- for each new token and K/V head, the pages of the cache
 // that score highest against the token's queries.
+//
+// score(p, g) = sum over the heads h of group g of q_h . kmean[p, g]: the
+// group's queries are added first, so a page costs one dot product of D.  Two
+// steps: k_scores forms every score in fp32 -- it reads the page means, which
+// is what bounds the call -- and k_pick, a block per (token, head), finds the
+// k-th largest and lists the pages.
+//
+// The choice has to be that of 64 bits.  An fp32 score is off by at most
+// E = gamma * |q|_1 * max|kmean| (standard bound of a sum of products), so a
+// page above (k-th + 2E) is in and one below (k-th - 2E) is out whatever the
+// rounding; if what lies between is more than is still wanted, those pages,
+// and only those, are scored again in 64 bits.  With scores that spread like
+// their terms that is a page in some thousand rows; rows whose bound is not
+// finite (fp32 overflows, a mean holds a NaN) take all their pages there.
 #include "cache.cuh"
 
 #include <algorithm>
@@ -7,86 +21,326 @@
 namespace gt {
 namespace {
 
-constexpr int kSelThreads = 128;
+struct SelArgs {
+    CacheView c;
+    CacheRows r;
+    const void* Q;
+    int* sel;
+    float2* score;     // [items, max_pages]: fp32 score and the largest |mean| of the page
+    float* qnorm;      // [items]: sum of |q| over the group
+    int H, G, n_sel;
+    int t0;            // first token of this pass
+    int chunks;        // blocks per item of k_scores
+    int q_vec;         // Q's rows are 16-byte aligned (and D a multiple of 8)
+};
 
-// score(p, g) = sum over the heads h of group g of q_h . kmean[p, g], in 64
-// bits; the token's own page is taken without a score, the n_sel - 1 others
-// by falling score (equal ones, and NaN as the lowest: by rising page).
-// Simplest form: a block per (token, K/V head), n_sel - 1 searches.
+constexpr int kScoreWarps = 4;
+constexpr int kScorePages = 128;     // pages of a block: 32 a warp, 8 at a time
+
+// Row of pass item i, its K/V head, request, position; false behind the last row.
+struct SelItem {
+    int t, g, s, pos, own;
+};
+__device__ __forceinline__ bool sel_item(const SelArgs& a, int64_t item, SelItem* it) {
+    it->t = a.t0 + static_cast<int>(item / a.c.Hkv);
+    it->g = static_cast<int>(item % a.c.Hkv);
+    if (it->t >= __ldg(a.r.tok_off + a.r.S)) return false;
+    it->s = request_of(a.r.tok_off, a.r.S, it->t);
+    it->pos = position_of(a.r, a.c.page, it->s, it->t);
+    it->own = it->pos < 0 ? -1 : it->pos >> a.c.lp;
+    return true;
+}
+
+// Four lanes hold a page's mean: lane cq takes the 16-byte pieces cq, cq + 4,
+// ... of it (NCH of them), eight pages a warp at a time; the lane's part of
+// the group's query stays in registers.
+template <typename T, int NCH>
+__global__ void __launch_bounds__(kScoreWarps * 32) k_scores(SelArgs a) {
+    const int64_t item = blockIdx.x / a.chunks;
+    const int p0 = static_cast<int>(blockIdx.x % a.chunks) * kScorePages;
+    SelItem it;
+    if (!sel_item(a, item, &it)) return;
+    // (a row that takes every page needs no score)
+    if (it.own <= a.n_sel - 1 || (p0 >= it.own && p0 > 0)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cq = lane & 3;
+    const CacheView& c = a.c;
+    const int D = c.D;
+    const bool vec = (D & 7) == 0;       // (means are 16-byte aligned, so are rows of 8 features)
+    float q[NCH][8], norm = 0.f;
+    const T* Q = static_cast<const T*>(a.Q) + (static_cast<int64_t>(it.t) * a.H + it.g * a.G) * D;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        const int d = (cq + 4 * i) * 8;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[i][k] = 0.f;
+        if (a.q_vec) {
+            if (d < D) {
+#pragma unroll 4
+                for (int h = 0; h < a.G; ++h) {
+                    Eight<T> e;
+                    e.load(Q + h * D + d);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        q[i][k] += e.x[k];
+                        norm += fabsf(e.x[k]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (d + k < D)
+                    for (int h = 0; h < a.G; ++h) {
+                        const float v = load_elem(Q, h * D + d + k);
+                        q[i][k] += v;
+                        norm += fabsf(v);
+                    }
+        }
+    }
+    if (p0 == 0 && warp == 0) {
+        norm += __shfl_xor_sync(0xffffffffu, norm, 1);
+        norm += __shfl_xor_sync(0xffffffffu, norm, 2);
+        if (lane == 0) a.qnorm[item] = norm;
+    }
+    const int* row = a.r.table + static_cast<int64_t>(it.s) * a.r.max_pages;
+    const int pw = p0 + warp * 32;
+    const int end = min(it.own, pw + 32);
+    const int id = pw + lane < end ? __ldg(row + pw + lane) : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int p = pw + u * 8 + (lane >> 2);
+        const int pid = __shfl_sync(0xffffffffu, id, u * 8 + (lane >> 2));
+        const bool ok = p < end && static_cast<unsigned>(pid) < static_cast<unsigned>(c.pages);
+        const __nv_bfloat16* m = c.kmean + (static_cast<int64_t>(ok ? pid : 0) * c.Hkv + it.g) * D;
+        uint4 w[NCH];
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int d = (cq + 4 * i) * 8;
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (ok && d < D) {
+                if (vec) {
+                    w[i] = __ldg(reinterpret_cast<const uint4*>(m + d));
+                } else {
+                    uint32_t* x = reinterpret_cast<uint32_t*>(&w[i]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (d + k < D)
+                            x[k >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(m[d + k])) << (16 * (k & 1));
+                }
+            }
+        }
+        float s = 0.f;
+        uint32_t big = 0;         // the largest |mean|, as bits, two at a time
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s = fmaf(q[i][2 * k], bf16lo(x[k]), s);
+                s = fmaf(q[i][2 * k + 1], bf16hi(x[k]), s);
+                big = __vmaxu2(big, x[k] & 0x7fff7fffu);
+            }
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        big = max(big & 0xffffu, big >> 16);
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        if (cq == 0 && p < end)
+            a.score[item * a.r.max_pages + p] = make_float2(s, __uint_as_float(big << 16));
+    }
+}
+
+constexpr int kPickThreads = 256;
+constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPickKeys = 8192;      // keys held in shared memory; rows of more pages read them again
+
+__device__ __forceinline__ uint32_t key_of(float x) {        // rises with x; -0 as 0
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return (u >> 31) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
+__device__ __forceinline__ unsigned long long key_of(double x) {
+    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
+    return (u >> 63) ? ~u : u | 0x8000000000000000ull;
+}
+
+// sum over the block; two barriers
+__device__ __forceinline__ int block_sum(int v, int* sums) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int x = 0;
+#pragma unroll
+    for (int w = 0; w < kPickWarps; ++w) x += sums[w];
+    return x;
+}
+
+// The k-th largest of key(0 .. n-1), bit by bit from the top: the largest
+// value that at least k keys reach.
+template <typename U, typename F> __device__ __forceinline__ U kth_largest(int n, int k, F key, int* sums) {
+    U v = 0;
+    for (U bit = U(1) << (8 * sizeof(U) - 1); bit; bit >>= 1) {
+        const U x = v | bit;
+        int cnt = 0;
+        for (int i = threadIdx.x; i < n; i += kPickThreads) cnt += key(i) >= x;
+        if (block_sum(cnt, sums) >= k) v = x;
+    }
+    return v;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kSelThreads)
-k_select(CacheView c, CacheRows r, const T* __restrict__ Q, int* __restrict__ sel, int H, int n_sel,
-         double* __restrict__ scratch, int n_items) {
+__global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items) {
+    __shared__ uint32_t keys[kPickKeys];
     __shared__ double qs[kCacheMaxD];
-    __shared__ double best_s[kSelThreads / 32];
-    __shared__ int best_i[kSelThreads / 32];
+    __shared__ int sums[kPickWarps];
+    __shared__ uint32_t s_big[kPickWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int end = r.tok_off[r.S];
-    const int G = H / c.Hkv;
-    double* score = scratch + (int64_t)blockIdx.x * r.max_pages;
-    for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
-        const int t = (int)(it / c.Hkv), g = (int)(it % c.Hkv);
-        if (t >= end) return;
-        const int s = request_of(r.tok_off, r.S, t);
-        const int pos = position_of(r, c.page, s, t);
-        int* out = sel + it * n_sel;
-        const int own = pos < 0 ? -1 : pos >> c.lp;
+    const int64_t item = blockIdx.x;
+    SelItem it;
+    if (item >= items || !sel_item(a, item, &it)) return;
+    const CacheView& c = a.c;
+    const int own = it.own, k = a.n_sel - 1;
+    int* out = a.sel + (static_cast<int64_t>(it.t) * c.Hkv + it.g) * a.n_sel;
+    if (own <= k) {                      // every page up to its own
+        for (int i = tid; i < a.n_sel; i += kPickThreads) out[i] = i <= own ? i : -1;
+        return;
+    }
+    // (own > k >= 0: k of the earlier pages, then its own)
+    if (tid == 0) out[k] = own;
+    if (k == 0) return;
+    float2* score = a.score + item * a.r.max_pages;
+    const bool held = own <= kPickKeys;
+    uint32_t bits = 0;                   // of the largest |mean| (a NaN is above all)
+    for (int i = tid; i < own; i += kPickThreads) {
+        const float2 x = score[i];
+        if (held) keys[i] = key_of(x.x);
+        bits = max(bits, __float_as_uint(x.y));
+    }
+    bits = __reduce_max_sync(0xffffffffu, bits);
+    if (lane == 0) s_big[warp] = bits;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPickWarps; ++w) bits = max(bits, s_big[w]);
+    const float big = __uint_as_float(bits);
+    // roundings of one score: G - 1 in the group's sum, D / 4 + 2 in the dot product, one each product
+    const float gamma = (a.G + c.D / 4 + 8) * 6.0e-8f * 1.01f;
+    const float norm = a.qnorm[item];
+    const float bound = 2.f * (gamma * norm * big) + 1e-36f;     // 2E; the last: products below fp32's range
+    auto key = [&](int i) { return held ? keys[i] : key_of(score[i].x); };
+    float lo = 0.f, hi = 0.f;
+    bool all = !(bound < 1e37f) || !(norm < 1e37f) || !(big < 1e37f) || !(norm * big < 1e37f);
+    bool redo = all;
+    if (!all) {
+        const float kth = key_value(kth_largest<uint32_t>(own, k, key, sums));
+        const float pad = bound + fabsf(kth) * 3e-7f;            // (and the rounding of these two)
+        lo = kth - pad;
+        hi = kth + pad;
+        int in = 0, mid = 0;
+        for (int i = tid; i < own; i += kPickThreads) {
+            const float x = key_value(key(i));
+            in += x > hi;
+            mid += x >= lo && x <= hi;
+        }
+        in = block_sum(in, sums);
+        mid = block_sum(mid, sums);
+        redo = mid != k - in;
+    }
+    unsigned long long edge = 0;       // redo: the k-th largest, and how many of that value are in
+    int ties = 0;
+    double* fine = reinterpret_cast<double*>(score);     // redo: a page's score in 64 bits, +inf: in, NaN: out
+    if (redo) {
         __syncthreads();
-        for (int d = tid; d < c.D; d += kSelThreads) {
+        for (int d = tid; d < c.D; d += kPickThreads) {
             double v = 0;
-            for (int h = 0; h < G; ++h) v += load_elem(Q, ((int64_t)t * H + g * G + h) * c.D + d);
+            for (int h = 0; h < a.G; ++h)
+                v += load_elem(static_cast<const T*>(a.Q), (static_cast<int64_t>(it.t) * a.H + it.g * a.G + h) * c.D + d);
             qs[d] = v;
         }
         __syncthreads();
-        for (int p = warp; p < own; p += kSelThreads / 32) {
-            const int pid = r.table[(int64_t)s * r.max_pages + p];
-            double v = 0;
-            if ((unsigned)pid < (unsigned)c.pages) {
-                const __nv_bfloat16* m = c.kmean + ((int64_t)pid * c.Hkv + g) * c.D;
-                for (int d = lane; d < c.D; d += 32) v += qs[d] * (double)__bfloat162float(m[d]);
-            }
+        const int* row = a.r.table + static_cast<int64_t>(it.s) * a.r.max_pages;
+        for (int i = warp; i < own; i += kPickWarps) {
+            const float x = score[i].x;
+            __syncwarp();
+            double v;
+            if (!all && x > hi) {
+                v = INFINITY;
+            } else if (!all && !(x >= lo)) {
+                v = NAN;
+            } else {
+                v = 0;
+                const int pid = __ldg(row + i);
+                if (static_cast<unsigned>(pid) < static_cast<unsigned>(c.pages)) {
+                    const __nv_bfloat16* m = c.kmean + (static_cast<int64_t>(pid) * c.Hkv + it.g) * c.D;
+                    for (int d = lane; d < c.D; d += 32) v = fma(qs[d], static_cast<double>(__bfloat162float(m[d])), v);
+                }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0) score[p] = v == v ? v : -INFINITY;
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (v != v) v = -INFINITY;
+            }
+            if (lane == 0) fine[i] = v;
         }
         __syncthreads();
-        const int k = min(own, n_sel - 1);   // earlier pages taken (own < 0: none)
-        for (int j = 0; j < k; ++j) {
-            double b = -INFINITY;
-            int bi = 0x7fffffff;
-            for (int p = tid; p < own; p += kSelThreads) {
-                const double v = score[p];
-                if (v == v && (v > b || bi == 0x7fffffff)) { b = v; bi = p; }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const double v = __shfl_xor_sync(0xffffffffu, b, o);
-                const int vi = __shfl_xor_sync(0xffffffffu, bi, o);
-                if (vi != 0x7fffffff && (bi == 0x7fffffff || v > b || (v == b && vi < bi))) { b = v; bi = vi; }
-            }
-            if (lane == 0) { best_s[warp] = b; best_i[warp] = bi; }
-            __syncthreads();
-            if (tid == 0) {
-                for (int w = 1; w < kSelThreads / 32; ++w)
-                    if (best_i[w] != 0x7fffffff &&
-                        (bi == 0x7fffffff || best_s[w] > b || (best_s[w] == b && best_i[w] < bi))) {
-                        b = best_s[w];
-                        bi = best_i[w];
-                    }
-                if (bi != 0x7fffffff) score[bi] = NAN;   // taken
-            }
-            __syncthreads();
-        }
-        // emit in rising order
-        if (tid == 0) {
-            int w = 0;
-            for (int p = 0; p < own && w < k; ++p)
-                if (score[p] != score[p]) out[w++] = p;
-            if (own >= 0 && w < n_sel) out[w++] = own;
-            for (; w < n_sel; ++w) out[w] = -1;
-        }
-        __syncthreads();
+        // (pages that are in by their fp32 scores rank before the others: +inf)
+        auto fkey = [&](int i) { const double v = fine[i]; return v != v ? 0ull : key_of(v); };
+        edge = kth_largest<unsigned long long>(own, k, fkey, sums);
+        int above = 0;
+        for (int i = tid; i < own; i += kPickThreads) above += fkey(i) > edge;
+        ties = k - block_sum(above, sums);
     }
+    // list them in rising order: 256 pages at a time
+    int at = 0, tied = 0;
+    for (int i0 = 0; i0 < own && at < k; i0 += kPickThreads) {
+        const int i = i0 + tid;
+        bool in = false, tie = false;
+        if (i < own) {
+            if (redo) {
+                const double v = fine[i];
+                const unsigned long long f = v != v ? 0ull : key_of(v);
+                in = f > edge;
+                tie = f == edge;
+            } else {
+                in = key_value(key(i)) >= lo;
+            }
+        }
+        if (redo) {                      // the first `ties` of the equal ones
+            const unsigned m = __ballot_sync(0xffffffffu, tie);
+            __syncthreads();
+            if (lane == 0) sums[warp] = __popc(m);
+            __syncthreads();
+            int before = tied, total = 0;
+#pragma unroll
+            for (int w = 0; w < kPickWarps; ++w) {
+                if (w < warp) before += sums[w];
+                total += sums[w];
+            }
+            before += __popc(m & ((1u << lane) - 1));
+            in |= tie && before < ties;
+            tied += total;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        __syncthreads();
+        if (lane == 0) sums[warp] = __popc(m);
+        __syncthreads();
+        int before = at, total = 0;
+#pragma unroll
+        for (int w = 0; w < kPickWarps; ++w) {
+            if (w < warp) before += sums[w];
+            total += sums[w];
+        }
+        before += __popc(m & ((1u << lane) - 1));
+        if (in && before < k) out[before] = i;
+        at += total;
+    }
+}
+
+template <typename T> void launch_scores(const SelArgs& a, int64_t blocks, cudaStream_t s) {
+    const unsigned n = static_cast<unsigned>(blocks);
+    if (a.c.D <= 32) k_scores<T, 1><<<n, kScoreWarps * 32, 0, s>>>(a);
+    else if (a.c.D <= 64) k_scores<T, 2><<<n, kScoreWarps * 32, 0, s>>>(a);
+    else if (a.c.D <= 128) k_scores<T, 4><<<n, kScoreWarps * 32, 0, s>>>(a);
+    else k_scores<T, 8><<<n, kScoreWarps * 32, 0, s>>>(a);
 }
 
 }  // namespace
@@ -98,33 +352,49 @@ extern "C" gtattn_status gtattn_cache_select(const gtattn_cache* cache, const vo
                                              const int32_t* length, const int32_t* tok_off, int32_t* sel, int64_t S,
                                              int64_t T, int64_t max_pages, int H, int n_sel, gtattn_dtype dtype,
                                              cudaStream_t stream) {
-    CacheView c;
-    CacheRows r;
-    GT_TRY(check_cache(cache, 2, &c));
-    GT_TRY(check_cache_rows(table, length, tok_off, S, T, max_pages, c.page, &r));
+    SelArgs a{};
+    GT_TRY(check_cache(cache, 2, &a.c));
+    GT_TRY(check_cache_rows(table, length, tok_off, S, T, max_pages, a.c.page, &a.r));
     if (dtype != GTATTN_F32 && dtype != GTATTN_BF16 && dtype != GTATTN_BF16_OUT_F32) return GTATTN_ERR_INVALID_ARG;
-    if (H < 1 || H > kCacheMaxHeads || H % c.Hkv || n_sel < 1 || n_sel > (1 << 20)) return GTATTN_ERR_INVALID_ARG;
+    if (H < 1 || H > kCacheMaxHeads || H % a.c.Hkv || n_sel < 1 || n_sel > (1 << 20)) return GTATTN_ERR_INVALID_ARG;
     if (T > 0 && (!Q || !sel)) return GTATTN_ERR_INVALID_ARG;
     const uintptr_t esz = dtype == GTATTN_F32 ? 4 : 2;
     if ((reinterpret_cast<uintptr_t>(Q) & (esz - 1)) || (reinterpret_cast<uintptr_t>(sel) & 3u))
         return GTATTN_ERR_INVALID_ARG;
-    if (T * c.Hkv >= (1ll << 31)) return GTATTN_ERR_UNSUPPORTED;
+    if (T * a.c.Hkv >= (1ll << 31)) return GTATTN_ERR_UNSUPPORTED;
     if (T == 0 || S == 0) return GTATTN_OK;
-    const int items = (int)(T * c.Hkv);
-    const int blocks = std::min(items, num_sms() * 8);
-    void* scratch = nullptr;
-    GT_TRY(pool_alloc(&scratch, sizeof(double) * (size_t)blocks * std::max<int64_t>(max_pages, 1), stream));
-    {
-        ProfScope ps(GTATTN_KCAT_CACHE, 1, stream);
-        if (dtype == GTATTN_F32)
-            k_select<float><<<blocks, kSelThreads, 0, stream>>>(c, r, static_cast<const float*>(Q), sel, H, n_sel,
-                                                                 static_cast<double*>(scratch), items);
-        else
-            k_select<__nv_bfloat16><<<blocks, kSelThreads, 0, stream>>>(c, r, static_cast<const __nv_bfloat16*>(Q),
-                                                                         sel, H, n_sel,
-                                                                         static_cast<double*>(scratch), items);
+    a.Q = Q;
+    a.sel = sel;
+    a.H = H;
+    a.G = H / a.c.Hkv;
+    a.q_vec = (a.c.D & 7) == 0 && (reinterpret_cast<uintptr_t>(Q) & 15u) == 0;
+    a.n_sel = n_sel;
+    // rows of at most n_sel pages take them all: nothing to score then
+    const bool score = max_pages > n_sel && n_sel > 1;
+    a.chunks = score ? (int)((max_pages + kScorePages - 1) / kScorePages) : 1;
+    // scores of as many tokens at a time as 256 MB hold (all, but for prompts over long requests)
+    const int64_t row = score ? (int64_t)a.c.Hkv * max_pages * sizeof(float2) : 1;
+    const int64_t tokens = std::max<int64_t>(1, std::min<int64_t>(T, score ? (256ll << 20) / row : T));
+    void* ws = nullptr;
+    if (score) {
+        GT_TRY(pool_alloc(&ws, (size_t)(tokens * row) + sizeof(float) * (size_t)tokens * a.c.Hkv, stream));
+        a.score = static_cast<float2*>(ws);
+        a.qnorm = reinterpret_cast<float*>(static_cast<char*>(ws) + tokens * row);
     }
-    const cudaError_t e = cudaGetLastError();
-    pool_free(scratch, stream);
+    cudaError_t e = cudaSuccess;
+    for (int64_t t0 = 0; t0 < T && e == cudaSuccess; t0 += tokens) {
+        a.t0 = (int)t0;
+        const int64_t items = std::min(tokens, T - t0) * a.c.Hkv;
+        ProfScope ps(GTATTN_KCAT_CACHE, score ? 2 : 1, stream);
+        if (dtype == GTATTN_F32) {
+            if (score) launch_scores<float>(a, items * a.chunks, stream);
+            k_pick<float><<<(unsigned)items, kPickThreads, 0, stream>>>(a, items);
+        } else {
+            if (score) launch_scores<__nv_bfloat16>(a, items * a.chunks, stream);
+            k_pick<__nv_bfloat16><<<(unsigned)items, kPickThreads, 0, stream>>>(a, items);
+        }
+        e = cudaGetLastError();
+    }
+    pool_free(ws, stream);
     return e == cudaSuccess ? GTATTN_OK : cuda_status(e);
 }
