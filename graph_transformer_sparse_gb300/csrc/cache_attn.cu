@@ -791,38 +791,56 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2) k_cache_attn_tile(CacheAtt
 }
 
 // Adds up the parts of the item that block blockIdx.x of the tile kernel ended
-// inside of: a warp per row, lanes over the features.
+// inside of, row blockIdx.y: each warp takes every kJoinWarps-th part, lanes
+// over the features; the warps' sums are added in warp order.  (A request
+// alone is cut into as many parts as there are blocks for its head; with one
+// warp a row this was 48 us for 76 parts, all of it latency.)
+constexpr int kJoinWarps = 8;
 template <typename TO, int D, int R>
-__global__ void __launch_bounds__(128) k_cache_join(CacheAttn a, TileWork wk) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_cache_join(CacheAttn a, TileWork wk) {
+    __shared__ float s_acc[kJoinWarps][D], s_sum[kJoinWarps], s_top[kJoinWarps];
     const JoinDesc jd = wk.join[blockIdx.x];
-    const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
     if (jd.parts == 0 || row >= jd.rows) return;
     auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * R + row; };
     float m = -INFINITY;
-    for (int i = lane; i < jd.parts; i += 32) m = fmaxf(m, wk.part_ml[slot(i)].x);
+    for (int i = threadIdx.x; i < jd.parts; i += kJoinWarps * 32) m = fmaxf(m, wk.part_ml[slot(i)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) s_top[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_top[w]);
     const float mu = m == -INFINITY ? 0.f : m;
     constexpr int V = D / 32;
     float acc[V], sum = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < jd.parts; ++i) {
+    for (int i = warp; i < jd.parts; i += kJoinWarps) {
         const float2 ml = wk.part_ml[slot(i)];
+        const float* p = wk.part_o + slot(i) * D;
         const float f = ex2(ml.x - mu);
         sum = fmaf(f, ml.y, sum);
-        const float* p = wk.part_o + slot(i) * D;
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = fmaf(f, p[v * 32 + lane], acc[v]);
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_acc[warp][v * 32 + lane] = acc[v];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d >= D) return;
+    float o = 0.f, total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        o += s_acc[w][d];
+        total += s_sum[w];
+    }
     const int q = jd.q0 + row;
     const int tok = a.sel ? 0 : q / a.G, hd = jd.head0 + (a.sel ? q : q % a.G);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        store_elem(static_cast<TO*>(a.out), (static_cast<int64_t>(jd.row0 + tok) * a.H + hd) * D + v * 32 + lane,
-                   acc[v] * inv);
+    store_elem(static_cast<TO*>(a.out), (static_cast<int64_t>(jd.row0 + tok) * a.H + hd) * D + d,
+               total == 0.f ? 0.f : o / total);
 }
 
 // ---- host -------------------------------------------------------------------
@@ -837,6 +855,7 @@ gtattn_status launch_tile(const CacheAttn& a, cudaStream_t s) {
     // (an item of one unit is never cut)
     const int64_t keys = a.sel ? (int64_t)a.n_sel * a.c.page : (int64_t)a.r.max_pages * a.c.page;
     const bool cut = keys > kUnit;
+    const unsigned rows = (unsigned)std::min<int64_t>(R, a.sel ? a.G : (int64_t)a.r.T * a.G);   // of a tile, at most
     TileWork wk{};
     const size_t n_o = cut ? sizeof(float) * 2 * blocks * R * D : 0, n_ml = cut ? sizeof(float2) * 2 * blocks * R : 0;
     void* ws = nullptr;
@@ -847,7 +866,7 @@ gtattn_status launch_tile(const CacheAttn& a, cudaStream_t s) {
     {
         ProfScope ps(GTATTN_KCAT_CACHE, cut ? 2 : 1, s);
         kernel<<<blocks, kTileWarps * 32, smem, s>>>(a, wk);
-        if (cut) k_cache_join<TO, D, R><<<dim3(blocks, R / 4), 128, 0, s>>>(a, wk);
+        if (cut) k_cache_join<TO, D, R><<<dim3(blocks, rows), kJoinWarps * 32, 0, s>>>(a, wk);
     }
     const cudaError_t e = cudaGetLastError();
     pool_free(ws, s);

@@ -190,6 +190,28 @@ template <typename U, typename F> __device__ __forceinline__ U kth_largest(int n
     return v;
 }
 
+// The group's queries added up in 64 bits (a block; a barrier has to follow).
+template <typename T> __device__ void query_sums(const SelArgs& a, const SelItem& it, double* qs) {
+    for (int d = threadIdx.x; d < a.c.D; d += kPickThreads) {
+        double v = 0;
+        for (int h = 0; h < a.G; ++h)
+            v += load_elem(static_cast<const T*>(a.Q), (static_cast<int64_t>(it.t) * a.H + it.g * a.G + h) * a.c.D + d);
+        qs[d] = v;
+    }
+}
+// Page p's score in 64 bits, NaN as -inf (a warp).
+__device__ __forceinline__ double exact_score(const SelArgs& a, const SelItem& it, const double* qs, int p, int lane) {
+    const int pid = __ldg(a.r.table + static_cast<int64_t>(it.s) * a.r.max_pages + p);
+    double v = 0;
+    if (static_cast<unsigned>(pid) < static_cast<unsigned>(a.c.pages)) {
+        const __nv_bfloat16* m = a.c.kmean + (static_cast<int64_t>(pid) * a.c.Hkv + it.g) * a.c.D;
+        for (int d = lane; d < a.c.D; d += 32) v = fma(qs[d], static_cast<double>(__bfloat162float(m[d])), v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v != v ? -INFINITY : v;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items) {
     __shared__ uint32_t keys[kPickKeys];
@@ -232,12 +254,13 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items)
     float lo = 0.f, hi = 0.f;
     bool all = !(bound < 1e37f) || !(norm < 1e37f) || !(big < 1e37f) || !(norm * big < 1e37f);
     bool redo = all;
+    int mid = 0, want = 0;               // pages between, and how many of them are in
     if (!all) {
         const float kth = key_value(kth_largest<uint32_t>(own, k, key, sums));
         const float pad = bound + fabsf(kth) * 3e-7f;            // (and the rounding of these two)
         lo = kth - pad;
         hi = kth + pad;
-        int in = 0, mid = 0;
+        int in = 0;
         for (int i = tid; i < own; i += kPickThreads) {
             const float x = key_value(key(i));
             in += x > hi;
@@ -245,21 +268,47 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items)
         }
         in = block_sum(in, sums);
         mid = block_sum(mid, sums);
-        redo = mid != k - in;
+        want = k - in;
+        redo = mid != want;
+    }
+    // few pages between (the usual case): each scored by a warp in 64 bits and
+    // ranked among them; its fp32 score then says in or out
+    const int few = all ? 0 : mid;
+    if (redo && few > 0 && few <= kPickThreads) {
+        __shared__ int z_at[kPickThreads];
+        __shared__ double z_score[kPickThreads];
+        __shared__ int z_n;
+        if (tid == 0) z_n = 0;
+        query_sums<T>(a, it, qs);
+        __syncthreads();
+        for (int i = tid; i < own; i += kPickThreads) {
+            const float x = key_value(key(i));
+            if (x >= lo && x <= hi) z_at[atomicAdd(&z_n, 1)] = i;
+        }
+        __syncthreads();
+        for (int z = warp; z < few; z += kPickWarps) {
+            const double v = exact_score(a, it, qs, z_at[z], lane);
+            if (lane == 0) z_score[z] = v;
+        }
+        __syncthreads();
+        if (tid < few) {
+            const double v = z_score[tid];
+            const int i = z_at[tid];
+            int rank = 0;
+            for (int z = 0; z < few; ++z) rank += z_score[z] > v || (z_score[z] == v && z_at[z] < i);
+            const float x = rank < want ? INFINITY : -INFINITY;
+            if (held) keys[i] = key_of(x);
+            else score[i].x = x;
+        }
+        __syncthreads();
+        redo = false;
     }
     unsigned long long edge = 0;       // redo: the k-th largest, and how many of that value are in
     int ties = 0;
     double* fine = reinterpret_cast<double*>(score);     // redo: a page's score in 64 bits, +inf: in, NaN: out
     if (redo) {
+        query_sums<T>(a, it, qs);
         __syncthreads();
-        for (int d = tid; d < c.D; d += kPickThreads) {
-            double v = 0;
-            for (int h = 0; h < a.G; ++h)
-                v += load_elem(static_cast<const T*>(a.Q), (static_cast<int64_t>(it.t) * a.H + it.g * a.G + h) * c.D + d);
-            qs[d] = v;
-        }
-        __syncthreads();
-        const int* row = a.r.table + static_cast<int64_t>(it.s) * a.r.max_pages;
         for (int i = warp; i < own; i += kPickWarps) {
             const float x = score[i].x;
             __syncwarp();
@@ -269,15 +318,7 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items)
             } else if (!all && !(x >= lo)) {
                 v = NAN;
             } else {
-                v = 0;
-                const int pid = __ldg(row + i);
-                if (static_cast<unsigned>(pid) < static_cast<unsigned>(c.pages)) {
-                    const __nv_bfloat16* m = c.kmean + (static_cast<int64_t>(pid) * c.Hkv + it.g) * c.D;
-                    for (int d = lane; d < c.D; d += 32) v = fma(qs[d], static_cast<double>(__bfloat162float(m[d])), v);
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (v != v) v = -INFINITY;
+                v = exact_score(a, it, qs, i, lane);
             }
             if (lane == 0) fine[i] = v;
         }
