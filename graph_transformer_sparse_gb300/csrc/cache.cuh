@@ -52,6 +52,19 @@ __device__ __forceinline__ int request_of(const int* __restrict__ tok_off, int S
     return lo;
 }
 
+// The same by a whole warp, 32 places a look.
+__device__ __forceinline__ int request_of_warp(const int* __restrict__ tok_off, int S, int t, int lane) {
+    int lo = 0, n = S;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const bool le = lane * step < n && __ldg(tok_off + lo + lane * step) <= t;
+        const int i = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+        lo += i * step;
+        n = min(step, n - i * step);
+    }
+    return lo;
+}
+
 // Position of row t of request s in its request; -1 when the request holds
 // fewer tokens than it has rows, capped at the table's last position.
 __device__ __forceinline__ int position_of(const CacheRows& r, int page, int s, int t) {

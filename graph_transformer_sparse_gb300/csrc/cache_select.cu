@@ -45,7 +45,7 @@ __device__ __forceinline__ bool sel_item(const SelArgs& a, int64_t item, SelItem
     it->t = a.t0 + static_cast<int>(item / a.c.Hkv);
     it->g = static_cast<int>(item % a.c.Hkv);
     if (it->t >= __ldg(a.r.tok_off + a.r.S)) return false;
-    it->s = request_of(a.r.tok_off, a.r.S, it->t);
+    it->s = request_of_warp(a.r.tok_off, a.r.S, it->t, threadIdx.x & 31);
     it->pos = position_of(a.r, a.c.page, it->s, it->t);
     it->own = it->pos < 0 ? -1 : it->pos >> a.c.lp;
     return true;
@@ -54,6 +54,91 @@ __device__ __forceinline__ bool sel_item(const SelArgs& a, int64_t item, SelItem
 // Four lanes hold a page's mean: lane cq takes the 16-byte pieces cq, cq + 4,
 // ... of it (NCH of them), eight pages a warp at a time; the lane's part of
 // the group's query stays in registers.
+template <typename T, int NCH> struct Query {
+    float q[NCH][8];
+    float norm;      // sum of |q| over the group (all four lanes)
+    __device__ __forceinline__ void load(const SelArgs& a, const SelItem& it, int cq) {
+        const int D = a.c.D;
+        const T* Q = static_cast<const T*>(a.Q) + (static_cast<int64_t>(it.t) * a.H + it.g * a.G) * D;
+        norm = 0.f;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int d = (cq + 4 * i) * 8;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) q[i][k] = 0.f;
+            if (a.q_vec) {
+                if (d < D) {
+#pragma unroll 4
+                    for (int h = 0; h < a.G; ++h) {
+                        Eight<T> e;
+                        e.load(Q + h * D + d);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            q[i][k] += e.x[k];
+                            norm += fabsf(e.x[k]);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (d + k < D)
+                        for (int h = 0; h < a.G; ++h) {
+                            const float v = load_elem(Q, h * D + d + k);
+                            q[i][k] += v;
+                            norm += fabsf(v);
+                        }
+            }
+        }
+        norm += __shfl_xor_sync(0xffffffffu, norm, 1);
+        norm += __shfl_xor_sync(0xffffffffu, norm, 2);
+    }
+};
+// One lane's pieces of a page's mean.
+template <int NCH> struct Mean {
+    uint4 w[NCH];
+    __device__ __forceinline__ void load(const SelArgs& a, const SelItem& it, int pid, bool ok, int cq) {
+        const int D = a.c.D;
+        ok = ok && static_cast<unsigned>(pid) < static_cast<unsigned>(a.c.pages);
+        const __nv_bfloat16* m = a.c.kmean + (static_cast<int64_t>(ok ? pid : 0) * a.c.Hkv + it.g) * D;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int d = (cq + 4 * i) * 8;
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (ok && d < D) {
+                if ((D & 7) == 0) {      // (means are 16-byte aligned, so are rows of 8 features)
+                    w[i] = __ldg(reinterpret_cast<const uint4*>(m + d));
+                } else {
+                    uint32_t* x = reinterpret_cast<uint32_t*>(&w[i]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (d + k < D) x[k >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(m[d + k])) << (16 * (k & 1));
+                }
+            }
+        }
+    }
+    // the score, and the bits of the largest |mean| (all four lanes)
+    template <typename T> __device__ __forceinline__ void score(const Query<T, NCH>& q, float& s, uint32_t& big) const {
+        s = 0.f;
+        big = 0;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s = fmaf(q.q[i][2 * k], bf16lo(x[k]), s);
+                s = fmaf(q.q[i][2 * k + 1], bf16hi(x[k]), s);
+                big = __vmaxu2(big, x[k] & 0x7fff7fffu);
+            }
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        big = max(big & 0xffffu, big >> 16);
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2)) << 16;
+    }
+};
+
 template <typename T, int NCH>
 __global__ void __launch_bounds__(kScoreWarps * 32) k_scores(SelArgs a) {
     const int64_t item = blockIdx.x / a.chunks;
@@ -63,97 +148,27 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_scores(SelArgs a) {
     // (a row that takes every page needs no score)
     if (it.own <= a.n_sel - 1 || (p0 >= it.own && p0 > 0)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cq = lane & 3;
-    const CacheView& c = a.c;
-    const int D = c.D;
-    const bool vec = (D & 7) == 0;       // (means are 16-byte aligned, so are rows of 8 features)
-    float q[NCH][8], norm = 0.f;
-    const T* Q = static_cast<const T*>(a.Q) + (static_cast<int64_t>(it.t) * a.H + it.g * a.G) * D;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        const int d = (cq + 4 * i) * 8;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) q[i][k] = 0.f;
-        if (a.q_vec) {
-            if (d < D) {
-#pragma unroll 4
-                for (int h = 0; h < a.G; ++h) {
-                    Eight<T> e;
-                    e.load(Q + h * D + d);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        q[i][k] += e.x[k];
-                        norm += fabsf(e.x[k]);
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (d + k < D)
-                    for (int h = 0; h < a.G; ++h) {
-                        const float v = load_elem(Q, h * D + d + k);
-                        q[i][k] += v;
-                        norm += fabsf(v);
-                    }
-        }
-    }
-    if (p0 == 0 && warp == 0) {
-        norm += __shfl_xor_sync(0xffffffffu, norm, 1);
-        norm += __shfl_xor_sync(0xffffffffu, norm, 2);
-        if (lane == 0) a.qnorm[item] = norm;
-    }
-    const int* row = a.r.table + static_cast<int64_t>(it.s) * a.r.max_pages;
-    const int pw = p0 + warp * 32;
-    const int end = min(it.own, pw + 32);
-    const int id = pw + lane < end ? __ldg(row + pw + lane) : -1;
+    const int pw = p0 + warp * 32, end = min(it.own, pw + 32);
+    const int id = pw + lane < end ? __ldg(a.r.table + static_cast<int64_t>(it.s) * a.r.max_pages + pw + lane) : -1;
+    Query<T, NCH> q;
+    q.load(a, it, cq);
+    if (p0 == 0 && threadIdx.x == 0) a.qnorm[item] = q.norm;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int p = pw + u * 8 + (lane >> 2);
-        const int pid = __shfl_sync(0xffffffffu, id, u * 8 + (lane >> 2));
-        const bool ok = p < end && static_cast<unsigned>(pid) < static_cast<unsigned>(c.pages);
-        const __nv_bfloat16* m = c.kmean + (static_cast<int64_t>(ok ? pid : 0) * c.Hkv + it.g) * D;
-        uint4 w[NCH];
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int d = (cq + 4 * i) * 8;
-            w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (ok && d < D) {
-                if (vec) {
-                    w[i] = __ldg(reinterpret_cast<const uint4*>(m + d));
-                } else {
-                    uint32_t* x = reinterpret_cast<uint32_t*>(&w[i]);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (d + k < D)
-                            x[k >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(m[d + k])) << (16 * (k & 1));
-                }
-            }
-        }
-        float s = 0.f;
-        uint32_t big = 0;         // the largest |mean|, as bits, two at a time
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s = fmaf(q[i][2 * k], bf16lo(x[k]), s);
-                s = fmaf(q[i][2 * k + 1], bf16hi(x[k]), s);
-                big = __vmaxu2(big, x[k] & 0x7fff7fffu);
-            }
-        }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        big = max(big & 0xffffu, big >> 16);
-        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        if (cq == 0 && p < end)
-            a.score[item * a.r.max_pages + p] = make_float2(s, __uint_as_float(big << 16));
+        Mean<NCH> m;
+        m.load(a, it, __shfl_sync(0xffffffffu, id, u * 8 + (lane >> 2)), p < end, cq);
+        float s;
+        uint32_t big;
+        m.score(q, s, big);
+        if (cq == 0 && p < end) a.score[item * a.r.max_pages + p] = make_float2(s, __uint_as_float(big));
     }
 }
 
-constexpr int kPickThreads = 256;
-constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kPickKeys = 8192;      // keys held in shared memory; rows of more pages read them again
+constexpr int kPickThreads = 256;    // of k_pick
+constexpr int kFusedThreads = 128;   // of k_select
+constexpr int kPickKeys = 8192;      // keys held in shared memory; k_pick reads those of rows of more pages again
+constexpr int kPickClose = 128;      // close pages ranked in shared memory
 
 __device__ __forceinline__ uint32_t key_of(float x) {        // rises with x; -0 as 0
     const uint32_t u = __float_as_uint(x + 0.f);
@@ -165,34 +180,56 @@ __device__ __forceinline__ unsigned long long key_of(double x) {
     return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
 
-// sum over the block; two barriers
-__device__ __forceinline__ int block_sum(int v, int* sums) {
-    v = __reduce_add_sync(0xffffffffu, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int x = 0;
+// Sums over the block, one barrier each: the partial sums alternate between
+// two places, so that the next call's do not meet this one's readers.
+template <int THREADS> struct BlockSum {
+    int (*at)[THREADS / 32];     // [2] in shared memory
+    int turn;
+    __device__ __forceinline__ int operator()(int v) {
+        v = __reduce_add_sync(0xffffffffu, v);
+        if ((threadIdx.x & 31) == 0) at[turn][threadIdx.x >> 5] = v;
+        __syncthreads();
+        int x = 0;
 #pragma unroll
-    for (int w = 0; w < kPickWarps; ++w) x += sums[w];
-    return x;
-}
+        for (int w = 0; w < THREADS / 32; ++w) x += at[turn][w];
+        turn ^= 1;
+        return x;
+    }
+    // sum over the warps before this one and over all, of one value a warp
+    __device__ __forceinline__ int before(int v, int* all) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 0) at[turn][warp] = v;
+        __syncthreads();
+        int x = 0, sum = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) x += at[turn][w];
+            sum += at[turn][w];
+        }
+        turn ^= 1;
+        *all = sum;
+        return x;
+    }
+};
 
 // The k-th largest of key(0 .. n-1), bit by bit from the top: the largest
-// value that at least k keys reach.
-template <typename U, typename F> __device__ __forceinline__ U kth_largest(int n, int k, F key, int* sums) {
-    U v = 0;
-    for (U bit = U(1) << (8 * sizeof(U) - 1); bit; bit >>= 1) {
+// value that at least k keys reach.  `top`: no key differs above this bit
+// from `common`, whose bits from it down are 0.
+template <int THREADS, typename U, typename F>
+__device__ __forceinline__ U kth_largest(int n, int k, U common, U top, F key, BlockSum<THREADS>& sum) {
+    U v = common;
+    for (U bit = top; bit; bit >>= 1) {
         const U x = v | bit;
         int cnt = 0;
-        for (int i = threadIdx.x; i < n; i += kPickThreads) cnt += key(i) >= x;
-        if (block_sum(cnt, sums) >= k) v = x;
+        for (int i = threadIdx.x; i < n; i += THREADS) cnt += key(i) >= x;
+        if (sum(cnt) >= k) v = x;
     }
     return v;
 }
 
 // The group's queries added up in 64 bits (a block; a barrier has to follow).
-template <typename T> __device__ void query_sums(const SelArgs& a, const SelItem& it, double* qs) {
-    for (int d = threadIdx.x; d < a.c.D; d += kPickThreads) {
+template <typename T, int THREADS> __device__ void query_sums(const SelArgs& a, const SelItem& it, double* qs) {
+    for (int d = threadIdx.x; d < a.c.D; d += THREADS) {
         double v = 0;
         for (int h = 0; h < a.G; ++h)
             v += load_elem(static_cast<const T*>(a.Q), (static_cast<int64_t>(it.t) * a.H + it.g * a.G + h) * a.c.D + d);
@@ -212,90 +249,93 @@ __device__ __forceinline__ double exact_score(const SelArgs& a, const SelItem& i
     return v != v ? -INFINITY : v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items) {
-    __shared__ uint32_t keys[kPickKeys];
+// Lists the k best of the row's `own` earlier pages (own > k > 0), by a block.
+// held: the fp32 scores' keys stand in keys[0 .. own), to be seen after a
+// barrier, else in score[].x.  bits: those of this thread's largest |mean|.
+// score: [max_pages] in global memory; with `held` only used, and written,
+// when many pages are close.
+template <typename T, int THREADS>
+__device__ __forceinline__ void pick_pages(const SelArgs& a, const SelItem& it, bool held, uint32_t* keys, float2* score,
+                                           uint32_t bits, float norm, int* out) {
+    constexpr int WARPS = THREADS / 32;
     __shared__ double qs[kCacheMaxD];
-    __shared__ int sums[kPickWarps];
-    __shared__ uint32_t s_big[kPickWarps];
+    __shared__ int s_sums[2][WARPS];
+    __shared__ uint32_t s_red[3][WARPS];
+    __shared__ int z_at[kPickClose];
+    __shared__ double z_score[kPickClose];
+    __shared__ int z_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t item = blockIdx.x;
-    SelItem it;
-    if (item >= items || !sel_item(a, item, &it)) return;
-    const CacheView& c = a.c;
     const int own = it.own, k = a.n_sel - 1;
-    int* out = a.sel + (static_cast<int64_t>(it.t) * c.Hkv + it.g) * a.n_sel;
-    if (own <= k) {                      // every page up to its own
-        for (int i = tid; i < a.n_sel; i += kPickThreads) out[i] = i <= own ? i : -1;
-        return;
-    }
-    // (own > k >= 0: k of the earlier pages, then its own)
-    if (tid == 0) out[k] = own;
-    if (k == 0) return;
-    float2* score = a.score + item * a.r.max_pages;
-    const bool held = own <= kPickKeys;
-    uint32_t bits = 0;                   // of the largest |mean| (a NaN is above all)
-    for (int i = tid; i < own; i += kPickThreads) {
-        const float2 x = score[i];
-        if (held) keys[i] = key_of(x.x);
-        bits = max(bits, __float_as_uint(x.y));
+    BlockSum<THREADS> sum{s_sums, 0};
+    auto key = [&](int i) { return held ? keys[i] : key_of(score[i].x); };
+    __syncthreads();
+    uint32_t any = 0, every = 0xffffffffu;
+    for (int i = tid; i < own; i += THREADS) {
+        const uint32_t x = key(i);
+        any |= x;
+        every &= x;
     }
     bits = __reduce_max_sync(0xffffffffu, bits);
-    if (lane == 0) s_big[warp] = bits;
+    any = __reduce_or_sync(0xffffffffu, any);
+    every = __reduce_and_sync(0xffffffffu, every);
+    if (lane == 0) {
+        s_red[0][warp] = bits;
+        s_red[1][warp] = any;
+        s_red[2][warp] = every;
+    }
+    if (tid == 0) z_n = 0;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kPickWarps; ++w) bits = max(bits, s_big[w]);
-    const float big = __uint_as_float(bits);
+    for (int w = 0; w < WARPS; ++w) {
+        bits = max(bits, s_red[0][w]);
+        any |= s_red[1][w];
+        every &= s_red[2][w];
+    }
+    const float big = __uint_as_float(bits);         // (a NaN's bits are above all)
     // roundings of one score: G - 1 in the group's sum, D / 4 + 2 in the dot product, one each product
-    const float gamma = (a.G + c.D / 4 + 8) * 6.0e-8f * 1.01f;
-    const float norm = a.qnorm[item];
+    const float gamma = (a.G + a.c.D / 4 + 8) * 6.0e-8f * 1.01f;
     const float bound = 2.f * (gamma * norm * big) + 1e-36f;     // 2E; the last: products below fp32's range
-    auto key = [&](int i) { return held ? keys[i] : key_of(score[i].x); };
     float lo = 0.f, hi = 0.f;
-    bool all = !(bound < 1e37f) || !(norm < 1e37f) || !(big < 1e37f) || !(norm * big < 1e37f);
+    const bool all = !(bound < 1e37f) || !(norm < 1e37f) || !(big < 1e37f) || !(norm * big < 1e37f);
     bool redo = all;
     int mid = 0, want = 0;               // pages between, and how many of them are in
     if (!all) {
-        const float kth = key_value(kth_largest<uint32_t>(own, k, key, sums));
+        const uint32_t differ = any ^ every;
+        const uint32_t top = differ ? 1u << (31 - __clz(differ)) : 0u;
+        const uint32_t common = top ? every & ~(2 * top - 1) : every;
+        const float kth = key_value(kth_largest<THREADS, uint32_t>(own, k, common, top, key, sum));
         const float pad = bound + fabsf(kth) * 3e-7f;            // (and the rounding of these two)
         lo = kth - pad;
         hi = kth + pad;
         int in = 0;
-        for (int i = tid; i < own; i += kPickThreads) {
+        for (int i = tid; i < own; i += THREADS) {
             const float x = key_value(key(i));
             in += x > hi;
-            mid += x >= lo && x <= hi;
+            if (x >= lo && x <= hi) {
+                ++mid;
+                const int z = atomicAdd(&z_n, 1);
+                if (z < kPickClose) z_at[z] = i;
+            }
         }
-        in = block_sum(in, sums);
-        mid = block_sum(mid, sums);
-        want = k - in;
+        want = k - sum(in);
+        mid = z_n;
         redo = mid != want;
     }
     // few pages between (the usual case): each scored by a warp in 64 bits and
     // ranked among them; its fp32 score then says in or out
-    const int few = all ? 0 : mid;
-    if (redo && few > 0 && few <= kPickThreads) {
-        __shared__ int z_at[kPickThreads];
-        __shared__ double z_score[kPickThreads];
-        __shared__ int z_n;
-        if (tid == 0) z_n = 0;
-        query_sums<T>(a, it, qs);
+    if (redo && !all && mid <= kPickClose) {
+        query_sums<T, THREADS>(a, it, qs);
         __syncthreads();
-        for (int i = tid; i < own; i += kPickThreads) {
-            const float x = key_value(key(i));
-            if (x >= lo && x <= hi) z_at[atomicAdd(&z_n, 1)] = i;
-        }
-        __syncthreads();
-        for (int z = warp; z < few; z += kPickWarps) {
+        for (int z = warp; z < mid; z += WARPS) {
             const double v = exact_score(a, it, qs, z_at[z], lane);
             if (lane == 0) z_score[z] = v;
         }
         __syncthreads();
-        if (tid < few) {
-            const double v = z_score[tid];
-            const int i = z_at[tid];
+        for (int y = tid; y < mid; y += THREADS) {
+            const double v = z_score[y];
+            const int i = z_at[y];
             int rank = 0;
-            for (int z = 0; z < few; ++z) rank += z_score[z] > v || (z_score[z] == v && z_at[z] < i);
+            for (int z = 0; z < mid; ++z) rank += z_score[z] > v || (z_score[z] == v && z_at[z] < i);
             const float x = rank < want ? INFINITY : -INFINITY;
             if (held) keys[i] = key_of(x);
             else score[i].x = x;
@@ -307,10 +347,10 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items)
     int ties = 0;
     double* fine = reinterpret_cast<double*>(score);     // redo: a page's score in 64 bits, +inf: in, NaN: out
     if (redo) {
-        query_sums<T>(a, it, qs);
+        query_sums<T, THREADS>(a, it, qs);
         __syncthreads();
-        for (int i = warp; i < own; i += kPickWarps) {
-            const float x = score[i].x;
+        for (int i = warp; i < own; i += WARPS) {
+            const float x = key_value(key(i));
             __syncwarp();
             double v;
             if (!all && x > hi) {
@@ -325,14 +365,14 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items)
         __syncthreads();
         // (pages that are in by their fp32 scores rank before the others: +inf)
         auto fkey = [&](int i) { const double v = fine[i]; return v != v ? 0ull : key_of(v); };
-        edge = kth_largest<unsigned long long>(own, k, fkey, sums);
+        edge = kth_largest<THREADS, unsigned long long>(own, k, 0ull, 1ull << 63, fkey, sum);
         int above = 0;
-        for (int i = tid; i < own; i += kPickThreads) above += fkey(i) > edge;
-        ties = k - block_sum(above, sums);
+        for (int i = tid; i < own; i += THREADS) above += fkey(i) > edge;
+        ties = k - sum(above);
     }
-    // list them in rising order: 256 pages at a time
+    // list them in rising order, THREADS pages at a time
     int at = 0, tied = 0;
-    for (int i0 = 0; i0 < own && at < k; i0 += kPickThreads) {
+    for (int i0 = 0; i0 < own && at < k; i0 += THREADS) {
         const int i = i0 + tid;
         bool in = false, tie = false;
         if (i < own) {
@@ -345,35 +385,100 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items)
                 in = key_value(key(i)) >= lo;
             }
         }
+        int total;
         if (redo) {                      // the first `ties` of the equal ones
             const unsigned m = __ballot_sync(0xffffffffu, tie);
-            __syncthreads();
-            if (lane == 0) sums[warp] = __popc(m);
-            __syncthreads();
-            int before = tied, total = 0;
-#pragma unroll
-            for (int w = 0; w < kPickWarps; ++w) {
-                if (w < warp) before += sums[w];
-                total += sums[w];
-            }
-            before += __popc(m & ((1u << lane) - 1));
+            const int before = tied + sum.before(__popc(m), &total) + __popc(m & ((1u << lane) - 1));
             in |= tie && before < ties;
             tied += total;
         }
         const unsigned m = __ballot_sync(0xffffffffu, in);
-        __syncthreads();
-        if (lane == 0) sums[warp] = __popc(m);
-        __syncthreads();
-        int before = at, total = 0;
-#pragma unroll
-        for (int w = 0; w < kPickWarps; ++w) {
-            if (w < warp) before += sums[w];
-            total += sums[w];
-        }
-        before += __popc(m & ((1u << lane) - 1));
+        const int before = at + sum.before(__popc(m), &total) + __popc(m & ((1u << lane) - 1));
         if (in && before < k) out[before] = i;
         at += total;
     }
+}
+
+// Rows that need no choice: every page up to their own, or their own alone.
+template <int THREADS> __device__ __forceinline__ bool pick_plain(const SelArgs& a, const SelItem& it, int* out) {
+    const int own = it.own, k = a.n_sel - 1;
+    if (own <= k) {
+        for (int i = threadIdx.x; i < a.n_sel; i += THREADS) out[i] = i <= own ? i : -1;
+        return true;
+    }
+    // (own > k >= 0: k of the earlier pages, then its own)
+    if (threadIdx.x == 0) out[k] = own;
+    return k == 0;
+}
+
+// The second step: a block per item, on the scores that k_scores left.
+template <typename T>
+__global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items) {
+    __shared__ uint32_t keys[kPickKeys];
+    const int64_t item = blockIdx.x;
+    SelItem it;
+    if (item >= items || !sel_item(a, item, &it)) return;
+    int* out = a.sel + (static_cast<int64_t>(it.t) * a.c.Hkv + it.g) * a.n_sel;
+    if (pick_plain<kPickThreads>(a, it, out)) return;
+    float2* score = a.score + item * a.r.max_pages;
+    const bool held = it.own <= kPickKeys;
+    uint32_t bits = 0;                   // of the largest |mean|
+    for (int i = threadIdx.x; i < it.own; i += kPickThreads) {
+        const float2 x = score[i];
+        if (held) keys[i] = key_of(x.x);
+        bits = max(bits, __float_as_uint(x.y));
+    }
+    pick_pages<T, kPickThreads>(a, it, held, keys, score, bits, a.qnorm[item], out);
+}
+
+// Both steps in one, a block per item: the scores go to shared memory.  For
+// many items or few pages; otherwise too few blocks would read the means.
+template <typename T, int NCH>
+__global__ void __launch_bounds__(kFusedThreads, NCH <= 4 ? 5 : 3) k_select(SelArgs a, int64_t items) {
+    extern __shared__ uint32_t dyn_keys[];
+    const int64_t item = blockIdx.x;
+    SelItem it;
+    if (item >= items || !sel_item(a, item, &it)) return;
+    int* out = a.sel + (static_cast<int64_t>(it.t) * a.c.Hkv + it.g) * a.n_sel;
+    if (pick_plain<kFusedThreads>(a, it, out)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cq = lane & 3;
+    const int* row = a.r.table + static_cast<int64_t>(it.s) * a.r.max_pages;
+    Query<T, NCH> q;
+    uint32_t bits = 0;
+    constexpr int STEP = kFusedThreads / 4, U = NCH <= 2 ? 4 : NCH == 4 ? 2 : 1;    // pages a block at once, times U
+    int p = warp * 8 + (lane >> 2);
+    int id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = p + u * STEP < it.own ? __ldg(row + p + u * STEP) : -1;
+    q.load(a, it, cq);
+    for (int p0 = 0; p0 < it.own; p0 += U * STEP, p += U * STEP) {       // (the same steps for every lane: shuffles)
+        Mean<NCH> m[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) m[u].load(a, it, id[u], p + u * STEP < it.own, cq);
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = p + (U + u) * STEP < it.own ? __ldg(row + p + (U + u) * STEP) : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float s;
+            uint32_t big;
+            m[u].score(q, s, big);
+            bits = max(bits, big);
+            if (cq == 0 && p + u * STEP < it.own) dyn_keys[p + u * STEP] = key_of(s);
+        }
+    }
+    pick_pages<T, kFusedThreads>(a, it, true, dyn_keys, a.score + item * a.r.max_pages, bits, q.norm, out);
+}
+
+template <typename T, int NCH> cudaError_t launch_fused(const SelArgs& a, int64_t items, cudaStream_t s) {
+    const int smem = std::min(a.r.max_pages, kPickKeys) * static_cast<int>(sizeof(uint32_t));
+    k_select<T, NCH><<<static_cast<unsigned>(items), kFusedThreads, smem, s>>>(a, items);
+    return cudaGetLastError();
+}
+template <typename T> cudaError_t launch_fused(const SelArgs& a, int64_t items, cudaStream_t s) {
+    if (a.c.D <= 32) return launch_fused<T, 1>(a, items, s);
+    if (a.c.D <= 64) return launch_fused<T, 2>(a, items, s);
+    if (a.c.D <= 128) return launch_fused<T, 4>(a, items, s);
+    return launch_fused<T, 8>(a, items, s);
 }
 
 template <typename T> void launch_scores(const SelArgs& a, int64_t blocks, cudaStream_t s) {
@@ -422,11 +527,19 @@ extern "C" gtattn_status gtattn_cache_select(const gtattn_cache* cache, const vo
         a.score = static_cast<float2*>(ws);
         a.qnorm = reinterpret_cast<float*>(static_cast<char*>(ws) + tokens * row);
     }
+    // One launch where the items alone give every SM a block or two, or a
+    // block's pages are few; the two steps otherwise (one request's 8 heads
+    // over thousands of pages).
     cudaError_t e = cudaSuccess;
     for (int64_t t0 = 0; t0 < T && e == cudaSuccess; t0 += tokens) {
         a.t0 = (int)t0;
         const int64_t items = std::min(tokens, T - t0) * a.c.Hkv;
-        ProfScope ps(GTATTN_KCAT_CACHE, score ? 2 : 1, stream);
+        const bool fused = max_pages <= kPickKeys && (items >= 2 * num_sms() || max_pages <= 512);
+        ProfScope ps(GTATTN_KCAT_CACHE, score && !fused ? 2 : 1, stream);
+        if (fused) {
+            e = dtype == GTATTN_F32 ? launch_fused<float>(a, items, stream) : launch_fused<__nv_bfloat16>(a, items, stream);
+            continue;
+        }
         if (dtype == GTATTN_F32) {
             if (score) launch_scores<float>(a, items * a.chunks, stream);
             k_pick<float><<<(unsigned)items, kPickThreads, 0, stream>>>(a, items);
