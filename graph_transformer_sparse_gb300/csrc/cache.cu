@@ -113,6 +113,8 @@ __device__ __forceinline__ long long slot_scan(long long v, long long* total) {
 __global__ void __launch_bounds__(kSlotThreads) k_slots(SlotsArgs a, int lp) {
     __shared__ long long s_tok[kSlotThreads + 1];                  // first token of each own request
     __shared__ int s_len[kSlotThreads], s_have[kSlotThreads], s_page[kSlotThreads];   // s_page: first new page; -1: refused
+    let_next_start();
+    after_previous();
     const int tid = threadIdx.x, s0 = blockIdx.x * kSlotThreads, s = s0 + tid;
     const bool lead = blockIdx.y == 0, final_block = blockIdx.x == gridDim.x - 1;
     int len = 0, add = 0, have = 0, need = 0, bad = 0;
@@ -223,6 +225,8 @@ __global__ void __launch_bounds__(kAppendThreads)
 k_append(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const int* __restrict__ slots, int T_rows) {
     __shared__ float red[kAppendThreads / 32];
     __shared__ int s_n;
+    let_next_start();
+    after_previous();
     const int t = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
     const bool is_v = blockIdx.z != 0;
     const int total = c.pages * c.page;
@@ -281,15 +285,12 @@ k_append(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const in
 // where most tokens begin no run.
 // Bound by memory: the new rows are read once from DRAM (the second pass over
 // them hits L1), a page's earlier keys are read for its mean.
-__device__ __forceinline__ uint2 eight_e4m3(const float (&x)[8]) {
+__device__ __forceinline__ uint2 eight_e4m3(const float (&x)[8], bool finite) {
     uint32_t h[4];
-    float worst = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i)
         h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-        worst = fmaxf(worst, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-    }
-    if (worst == INFINITY) {     // (a NaN converts to NaN by itself)
+    if (!finite) {               // (a NaN converts to NaN by itself, an infinity would to 448)
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = f32_e4m3(x[2 * i]) | (f32_e4m3(x[2 * i + 1]) << 8);
     }
@@ -305,12 +306,32 @@ __device__ __forceinline__ void eight_f32(uint2 c, float (&x)[8]) {
     }
 }
 
+// The largest |x| of eight as bits (what is not finite is at or above 0x7f800000).
+__device__ __forceinline__ uint32_t eight_top(const float (&x)[8]) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t = max(t, __float_as_uint(x[k]) & 0x7fffffffu);
+    return t;
+}
+// The same of the finite ones.
+__device__ __forceinline__ uint32_t eight_finite_top(const float (&x)[8]) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t u = __float_as_uint(x[k]) & 0x7fffffffu;
+        if (u < 0x7f800000u) t = max(t, u);
+    }
+    return t;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads)
 k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const int* __restrict__ slots, int T_rows,
           int span, int l8) {       // l8 = log2(D / 8)
-    __shared__ float red[kAppendThreads / 32];
+    __shared__ uint32_t red[kAppendThreads / 32];
     __shared__ float cols[kCacheMaxD];
+    let_next_start();
+    after_previous();
     const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     const bool is_v = blockIdx.z != 0;
     const int D = c.D, HD = c.Hkv * D, W = 1 << l8;
@@ -344,27 +365,38 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
         float* sp = (is_v ? c.vscale : c.kscale) + ph;
         uint8_t* tile = (is_v ? c.v8 : c.k8) + (ph << c.lp) * D + cc * 8;
         const float old = f > 0 ? *sp : 0.f;
-        float amax = 0.f;
+        uint32_t top = 0;
 #pragma unroll 4
         for (int i = rr; i < n; i += rows) {
             Eight<T> e;
             e.load(x + static_cast<int64_t>(i) * HD);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float v = fabsf(e.x[k]);
-                if (v < INFINITY) amax = fmaxf(amax, v);
-            }
+            top = max(top, eight_top(e.x));
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        top = __reduce_max_sync(0xffffffffu, top);
         __syncthreads();                                    // (red and cols of the run before are read)
-        if (lane == 0) red[tid >> 5] = amax;
+        if (lane == 0) red[tid >> 5] = top;
         const bool mean = !is_v && c.kmean;
         if (mean)
             for (int d = tid; d < D; d += kAppendThreads) cols[d] = 0.f;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
+        for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, red[w]);
+        const bool finite = top < 0x7f800000u;
+        if (!finite) {                                      // once more, of the finite ones
+            top = 0;
+            for (int i = rr; i < n; i += rows) {
+                Eight<T> e;
+                e.load(x + static_cast<int64_t>(i) * HD);
+                top = max(top, eight_finite_top(e.x));
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            __syncthreads();
+            if (lane == 0) red[tid >> 5] = top;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, red[w]);
+        }
+        const float amax = __uint_as_float(top);
         const float now = fmaxf(old, power_scale(amax));
         float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         const bool grown = f > 0 && now != old;
@@ -379,7 +411,7 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
                 if (grown) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) y[k] *= ratio;
-                    code = eight_e4m3(y);
+                    code = eight_e4m3(y, true);
                     *p = code;
                     eight_f32(code, y);
                 }
@@ -394,7 +426,7 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
             e.load(x + static_cast<int64_t>(i) * HD);
 #pragma unroll
             for (int k = 0; k < 8; ++k) e.x[k] *= inv;
-            const uint2 code = eight_e4m3(e.x);
+            const uint2 code = eight_e4m3(e.x, finite);
             *reinterpret_cast<uint2*>(tile + (f + i) * D) = code;
             if (mean) {
                 float y[8];
@@ -445,8 +477,7 @@ extern "C" gtattn_status gtattn_cache_slots(const int32_t* length, const int32_t
     const int groups = std::max<int>(1, (int)((S + kSlotThreads - 1) / kSlotThreads));
     // blocks of a group: about 1024 tokens each, all groups within a wave or two
     const int share = (int)std::min<int64_t>(std::max<int64_t>(1, T / groups / 1024), std::max(1, 4 * num_sms() / groups));
-    k_slots<<<dim3(groups, share), kSlotThreads, 0, stream>>>(a, page == 16 ? 4 : page == 32 ? 5 : 6);
-    GT_CUDA(cudaGetLastError());
+    GT_CUDA(launch_after(k_slots, dim3(groups, share), kSlotThreads, 0, stream, a, page == 16 ? 4 : page == 32 ? 5 : 6));
     return GTATTN_OK;
 }
 
@@ -472,23 +503,19 @@ extern "C" gtattn_status gtattn_cache_append(const gtattn_cache* cache, const vo
         const int64_t per_sm16 = T * c.Hkv * 2 / (16 * num_sms());
         const int span = (int)std::min<int64_t>(32, std::max<int64_t>(1, per_sm16));
         const dim3 grid((unsigned)((T + span - 1) / span), c.Hkv, 2);
-        if (dtype == GTATTN_F32)
-            k_append8<float><<<grid, kAppendThreads, 0, stream>>>(c, static_cast<const float*>(K),
-                                                                   static_cast<const float*>(V), slots, (int)T, span, l8);
-        else
-            k_append8<__nv_bfloat16><<<grid, kAppendThreads, 0, stream>>>(
-                c, static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), slots, (int)T, span, l8);
-        GT_CUDA(cudaGetLastError());
+        GT_CUDA(dtype == GTATTN_F32
+                    ? launch_after(k_append8<float>, grid, kAppendThreads, 0, stream, c, static_cast<const float*>(K),
+                                   static_cast<const float*>(V), slots, (int)T, span, l8)
+                    : launch_after(k_append8<__nv_bfloat16>, grid, kAppendThreads, 0, stream, c,
+                                   static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), slots, (int)T,
+                                   span, l8));
         return GTATTN_OK;
     }
     const dim3 grid((unsigned)T, c.Hkv, 2);
-    if (dtype == GTATTN_F32)
-        k_append<float><<<grid, kAppendThreads, 0, stream>>>(c, static_cast<const float*>(K),
-                                                              static_cast<const float*>(V), slots, (int)T);
-    else
-        k_append<__nv_bfloat16><<<grid, kAppendThreads, 0, stream>>>(c, static_cast<const __nv_bfloat16*>(K),
-                                                                      static_cast<const __nv_bfloat16*>(V), slots,
-                                                                      (int)T);
-    GT_CUDA(cudaGetLastError());
+    GT_CUDA(dtype == GTATTN_F32
+                ? launch_after(k_append<float>, grid, kAppendThreads, 0, stream, c, static_cast<const float*>(K),
+                               static_cast<const float*>(V), slots, (int)T)
+                : launch_after(k_append<__nv_bfloat16>, grid, kAppendThreads, 0, stream, c,
+                               static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), slots, (int)T));
     return GTATTN_OK;
 }

@@ -30,6 +30,8 @@ template <typename TI, typename TO>
 __global__ void __launch_bounds__(kGenWarps * 32) k_cache_attn_generic(CacheAttn a, int64_t n_items) {
     __shared__ float sm_acc[kGenWarps][kCacheMaxD];
     __shared__ float sm_m[kGenWarps], sm_l[kGenWarps];
+    let_next_start();
+    after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const CacheView& c = a.c;
     const int end = a.r.tok_off[a.r.S];
@@ -432,7 +434,8 @@ __device__ __forceinline__ Task part_of(const Item& it, unsigned slot, int lc, i
 __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheAttn a, TileWork wk, int R) {
     __shared__ int held[3 * kPlanHeld];
     __shared__ int s_most[kPlanThreads / 32];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
+    after_previous();
     const int S = a.r.S, tid = threadIdx.x;
     const long long x0 = static_cast<long long>(blockIdx.x) * kPlanThreads + tid;
     const long long dx = static_cast<long long>(gridDim.x) * kPlanThreads;
@@ -588,8 +591,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cac
     const int Hkv = c.Hkv, page = c.page;
     uint8_t* ring = smem + warp * NST * STAGE;
     const uint32_t ring_u = smem_u32(ring);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next_start();
+    after_previous();
 
     const unsigned tasks = wk.plan ? wk.plan->tasks : 0;
     // Task i of this block (0: by its place in the grid, others claimed) goes to sm_task by way of warp 0's
@@ -1030,7 +1033,8 @@ constexpr int kJoinFew = 16;
 template <typename TO, int D, int R>
 __global__ void __launch_bounds__(kJoinWarps * 32, 2) k_cache_join(CacheAttn a, TileWork wk) {
     __shared__ float s_acc[kJoinWarps][D], s_sum[kJoinWarps], s_top[kJoinWarps];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next_start();
+    after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned items = wk.plan->multi;
     const bool longer = wk.plan->most > kJoinFew;
@@ -1116,23 +1120,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) k_cache_join(CacheAttn a, 
 }
 
 // ---- host -------------------------------------------------------------------
-// A kernel whose blocks may start while the one before it in the stream ends;
-// it waits for that one's results itself (griddepcontrol.wait).
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-}
-
 template <typename TI, typename TO, int D, int NT, bool SPLITQ, bool SPLITP>
 gtattn_status launch_tile(const CacheAttn& a, cudaStream_t s) {
     constexpr int R = 8 * NT, smem = tile_smem<D, NT>();
@@ -1148,8 +1135,7 @@ gtattn_status launch_tile(const CacheAttn& a, cudaStream_t s) {
     TileWork wk{};
     if (!cut && items <= blocks) {
         ProfScope ps(GTATTN_KCAT_CACHE, 1, s);
-        kernel<<<(unsigned)items, kTileWarps * 32, smem, s>>>(a, wk);
-        GT_CUDA(cudaGetLastError());
+        GT_CUDA(launch_after(kernel, dim3((unsigned)items), kTileWarps * 32, smem, s, a, wk));
         return GTATTN_OK;
     }
     wk.target = kTasksPerBlock * blocks;
@@ -1171,8 +1157,8 @@ gtattn_status launch_tile(const CacheAttn& a, cudaStream_t s) {
     {
         ProfScope ps(GTATTN_KCAT_CACHE, cut ? 3 : 2, s);
         const int64_t list = items + (int64_t)slots;        // tasks, at most
-        k_cache_plan<<<(unsigned)std::min<int64_t>(num_sms(), (list + 2 * kPlanThreads - 1) / (2 * kPlanThreads)), kPlanThreads, 0, s>>>(a, wk, R);
-        e = cudaGetLastError();
+        e = launch_after(k_cache_plan, dim3((unsigned)std::min<int64_t>(num_sms(), (list + 2 * kPlanThreads - 1) / (2 * kPlanThreads))),
+                         kPlanThreads, 0, s, a, wk, R);
         if (e == cudaSuccess)
             e = launch_after(kernel, dim3((unsigned)(cut ? blocks : std::min<int64_t>(blocks, items))), kTileWarps * 32, smem, s, a, wk);
         if (cut && e == cudaSuccess) {
@@ -1244,12 +1230,9 @@ extern "C" gtattn_status gtattn_fwd_cache(const gtattn_cache* cache, const void*
     const int64_t items = T * H;
     const int blocks = (int)std::min<int64_t>(items, num_sms() * 16);
     ProfScope ps(GTATTN_KCAT_CACHE, 1, stream);
-    if (dtype == GTATTN_F32)
-        k_cache_attn_generic<float, float><<<blocks, kGenWarps * 32, 0, stream>>>(a, items);
-    else if (dtype == GTATTN_BF16)
-        k_cache_attn_generic<__nv_bfloat16, __nv_bfloat16><<<blocks, kGenWarps * 32, 0, stream>>>(a, items);
-    else
-        k_cache_attn_generic<__nv_bfloat16, float><<<blocks, kGenWarps * 32, 0, stream>>>(a, items);
-    GT_CUDA(cudaGetLastError());
+    using B = __nv_bfloat16;
+    const auto kernel = dtype == GTATTN_F32 ? k_cache_attn_generic<float, float>
+                        : dtype == GTATTN_BF16 ? k_cache_attn_generic<B, B> : k_cache_attn_generic<B, float>;
+    GT_CUDA(launch_after(kernel, dim3(blocks), kGenWarps * 32, 0, stream, a, items));
     return GTATTN_OK;
 }

@@ -141,6 +141,8 @@ template <int NCH> struct Mean {
 
 template <typename T, int NCH>
 __global__ void __launch_bounds__(kScoreWarps * 32) k_scores(SelArgs a) {
+    let_next_start();
+    after_previous();
     const int64_t item = blockIdx.x / a.chunks;
     const int p0 = static_cast<int>(blockIdx.x % a.chunks) * kScorePages;
     SelItem it;
@@ -214,15 +216,31 @@ template <int THREADS> struct BlockSum {
 
 // The k-th largest of key(0 .. n-1), bit by bit from the top: the largest
 // value that at least k keys reach.  `top`: no key differs above this bit
-// from `common`, whose bits from it down are 0.
+// from `common`, whose bits from it down are 0.  Where exactly k keys reach a
+// value the least of them is it (half the bits on average).
 template <int THREADS, typename U, typename F>
-__device__ __forceinline__ U kth_largest(int n, int k, U common, U top, F key, BlockSum<THREADS>& sum) {
+__device__ __forceinline__ U kth_largest(int n, int k, U common, U top, F key, BlockSum<THREADS>& sum, U* least) {
     U v = common;
     for (U bit = top; bit; bit >>= 1) {
         const U x = v | bit;
         int cnt = 0;
         for (int i = threadIdx.x; i < n; i += THREADS) cnt += key(i) >= x;
-        if (sum(cnt) >= k) v = x;
+        cnt = sum(cnt);
+        if (cnt >= k) v = x;
+        if (cnt == k) {
+            U m = ~U(0);
+            for (int i = threadIdx.x; i < n; i += THREADS) {
+                const U y = key(i);
+                if (y >= x) m = min(m, y);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = min(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if ((threadIdx.x & 31) == 0) least[threadIdx.x >> 5] = m;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < THREADS / 32; ++w) m = min(m, least[w]);
+            return m;
+        }
     }
     return v;
 }
@@ -261,6 +279,7 @@ __device__ __forceinline__ void pick_pages(const SelArgs& a, const SelItem& it, 
     __shared__ double qs[kCacheMaxD];
     __shared__ int s_sums[2][WARPS];
     __shared__ uint32_t s_red[3][WARPS];
+    __shared__ unsigned long long s_least[WARPS];
     __shared__ int z_at[kPickClose];
     __shared__ double z_score[kPickClose];
     __shared__ int z_n;
@@ -303,7 +322,7 @@ __device__ __forceinline__ void pick_pages(const SelArgs& a, const SelItem& it, 
         const uint32_t differ = any ^ every;
         const uint32_t top = differ ? 1u << (31 - __clz(differ)) : 0u;
         const uint32_t common = top ? every & ~(2 * top - 1) : every;
-        const float kth = key_value(kth_largest<THREADS, uint32_t>(own, k, common, top, key, sum));
+        const float kth = key_value(kth_largest<THREADS, uint32_t>(own, k, common, top, key, sum, s_red[0]));
         const float pad = bound + fabsf(kth) * 3e-7f;            // (and the rounding of these two)
         lo = kth - pad;
         hi = kth + pad;
@@ -365,7 +384,7 @@ __device__ __forceinline__ void pick_pages(const SelArgs& a, const SelItem& it, 
         __syncthreads();
         // (pages that are in by their fp32 scores rank before the others: +inf)
         auto fkey = [&](int i) { const double v = fine[i]; return v != v ? 0ull : key_of(v); };
-        edge = kth_largest<THREADS, unsigned long long>(own, k, 0ull, 1ull << 63, fkey, sum);
+        edge = kth_largest<THREADS, unsigned long long>(own, k, 0ull, 1ull << 63, fkey, sum, s_least);
         int above = 0;
         for (int i = tid; i < own; i += THREADS) above += fkey(i) > edge;
         ties = k - sum(above);
@@ -415,6 +434,8 @@ template <int THREADS> __device__ __forceinline__ bool pick_plain(const SelArgs&
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items) {
     __shared__ uint32_t keys[kPickKeys];
+    let_next_start();
+    after_previous();
     const int64_t item = blockIdx.x;
     SelItem it;
     if (item >= items || !sel_item(a, item, &it)) return;
@@ -436,6 +457,8 @@ __global__ void __launch_bounds__(kPickThreads) k_pick(SelArgs a, int64_t items)
 template <typename T, int NCH>
 __global__ void __launch_bounds__(kFusedThreads, NCH <= 4 ? 5 : 3) k_select(SelArgs a, int64_t items) {
     extern __shared__ uint32_t dyn_keys[];
+    let_next_start();
+    after_previous();
     const int64_t item = blockIdx.x;
     SelItem it;
     if (item >= items || !sel_item(a, item, &it)) return;
@@ -469,24 +492,22 @@ __global__ void __launch_bounds__(kFusedThreads, NCH <= 4 ? 5 : 3) k_select(SelA
     pick_pages<T, kFusedThreads>(a, it, true, dyn_keys, a.score + item * a.r.max_pages, bits, q.norm, out);
 }
 
-template <typename T, int NCH> cudaError_t launch_fused(const SelArgs& a, int64_t items, cudaStream_t s) {
-    const int smem = std::min(a.r.max_pages, kPickKeys) * static_cast<int>(sizeof(uint32_t));
-    k_select<T, NCH><<<static_cast<unsigned>(items), kFusedThreads, smem, s>>>(a, items);
-    return cudaGetLastError();
+template <typename T> cudaError_t launch_scores(const SelArgs& a, int64_t blocks, cudaStream_t s) {
+    const auto kernel = a.c.D <= 32 ? k_scores<T, 1> : a.c.D <= 64 ? k_scores<T, 2> : a.c.D <= 128 ? k_scores<T, 4> : k_scores<T, 8>;
+    return launch_after(kernel, dim3(static_cast<unsigned>(blocks)), kScoreWarps * 32, 0, s, a);
 }
-template <typename T> cudaError_t launch_fused(const SelArgs& a, int64_t items, cudaStream_t s) {
-    if (a.c.D <= 32) return launch_fused<T, 1>(a, items, s);
-    if (a.c.D <= 64) return launch_fused<T, 2>(a, items, s);
-    if (a.c.D <= 128) return launch_fused<T, 4>(a, items, s);
-    return launch_fused<T, 8>(a, items, s);
-}
-
-template <typename T> void launch_scores(const SelArgs& a, int64_t blocks, cudaStream_t s) {
-    const unsigned n = static_cast<unsigned>(blocks);
-    if (a.c.D <= 32) k_scores<T, 1><<<n, kScoreWarps * 32, 0, s>>>(a);
-    else if (a.c.D <= 64) k_scores<T, 2><<<n, kScoreWarps * 32, 0, s>>>(a);
-    else if (a.c.D <= 128) k_scores<T, 4><<<n, kScoreWarps * 32, 0, s>>>(a);
-    else k_scores<T, 8><<<n, kScoreWarps * 32, 0, s>>>(a);
+template <typename T> cudaError_t launch_select(const SelArgs& a, int64_t items, bool score, bool fused, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(items));
+    if (fused) {
+        const auto kernel = a.c.D <= 32 ? k_select<T, 1> : a.c.D <= 64 ? k_select<T, 2> : a.c.D <= 128 ? k_select<T, 4> : k_select<T, 8>;
+        const int smem = std::min(a.r.max_pages, kPickKeys) * static_cast<int>(sizeof(uint32_t));
+        return launch_after(kernel, grid, kFusedThreads, smem, s, a, items);
+    }
+    if (score) {
+        const cudaError_t e = launch_scores<T>(a, items * a.chunks, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_after(k_pick<T>, grid, kPickThreads, 0, s, a, items);
 }
 
 }  // namespace
@@ -536,18 +557,8 @@ extern "C" gtattn_status gtattn_cache_select(const gtattn_cache* cache, const vo
         const int64_t items = std::min(tokens, T - t0) * a.c.Hkv;
         const bool fused = max_pages <= kPickKeys && (items >= 2 * num_sms() || max_pages <= 512);
         ProfScope ps(GTATTN_KCAT_CACHE, score && !fused ? 2 : 1, stream);
-        if (fused) {
-            e = dtype == GTATTN_F32 ? launch_fused<float>(a, items, stream) : launch_fused<__nv_bfloat16>(a, items, stream);
-            continue;
-        }
-        if (dtype == GTATTN_F32) {
-            if (score) launch_scores<float>(a, items * a.chunks, stream);
-            k_pick<float><<<(unsigned)items, kPickThreads, 0, stream>>>(a, items);
-        } else {
-            if (score) launch_scores<__nv_bfloat16>(a, items * a.chunks, stream);
-            k_pick<__nv_bfloat16><<<(unsigned)items, kPickThreads, 0, stream>>>(a, items);
-        }
-        e = cudaGetLastError();
+        e = dtype == GTATTN_F32 ? launch_select<float>(a, items, score, fused, stream)
+                                : launch_select<__nv_bfloat16>(a, items, score, fused, stream);
     }
     pool_free(ws, stream);
     return e == cudaSuccess ? GTATTN_OK : cuda_status(e);
