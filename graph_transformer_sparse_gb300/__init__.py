@@ -452,6 +452,8 @@ def _arg(x, name, least, dtypes, dev):
     least ``least`` elements of one of ``dtypes`` (ints pass as pointers)."""
     if x is None or isinstance(x, int):
         return x
+    if x.dtype in dtypes and x.numel() >= least and x.is_contiguous() and x.get_device() == dev:
+        return x.data_ptr() or None
     if x.dtype not in dtypes:
         raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
     n = x.numel()
@@ -464,31 +466,26 @@ def _arg(x, name, least, dtypes, dev):
     return x.data_ptr() or None
 
 
-def _call_dev(cache=None):
-    """Current CUDA device, on which the calls run; the cache has to be on it."""
+_types_of = None       # gtattn_dtype -> (input, output) torch dtypes; None -> int32's; as tuples for _arg
+
+
+def _call(cache, dtype, stream):
+    """(library, current device, int32, input and output types, stream) of a
+    cache call; the cache has to be on the current device."""
+    global _types_of
     import torch
+    if _types_of is None:
+        f, b = (torch.float32,), (torch.bfloat16,)
+        _types_of = {None: (None, None), GTATTN_F32: (f, f), GTATTN_BF16: (b, b), GTATTN_BF16_OUT_F32: (b, f),
+                     "i32": (torch.int32,)}
+    if dtype not in _types_of:
+        raise GtattnError(GTATTN_ERR_INVALID_ARG, "dtype")
     dev = torch.cuda.current_device()
     if cache is not None and cache._dev != dev:
         raise ValueError(f"the cache is on {cache.device}, the call runs on cuda:{dev}")
-    return dev
-
-
-def _types(dtype):
-    """(input, output) torch dtypes of a gtattn_dtype, as tuples for _arg."""
-    import torch
-    f, b = (torch.float32,), (torch.bfloat16,)
-    if dtype == GTATTN_F32:
-        return f, f
-    if dtype == GTATTN_BF16:
-        return b, b
-    if dtype == GTATTN_BF16_OUT_F32:
-        return b, f
-    raise GtattnError(GTATTN_ERR_INVALID_ARG, "dtype")
-
-
-def _i32():
-    import torch
-    return (torch.int32,)
+    ti, to = _types_of[dtype]
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return _lib or load(), dev, _types_of["i32"], ti, to, s
 
 
 def gtattn_cache_slots(length, add, table, free_pages, new_length, tok_off, slots, counts, S, max_pages, n_free, T, page,
@@ -497,33 +494,32 @@ def gtattn_cache_slots(length, add, table, free_pages, new_length, tok_off, slot
     ``free_pages`` into ``table`` [S, max_pages], writes ``new_length`` [S],
     ``tok_off`` [S+1], ``slots`` [T] (-1: no place) and ``counts`` [3] (pages
     taken, rows, requests refused); all int32 CUDA tensors."""
-    dev, i = _call_dev(), _i32()
-    _check(load().gtattn_cache_slots(
+    lib, dev, i, _, _, stream = _call(None, None, stream)
+    _check(lib.gtattn_cache_slots(
         _arg(length, "length", S, i, dev), _arg(add, "add", S, i, dev), _arg(table, "table", S * max_pages, i, dev),
         _arg(free_pages, "free_pages", n_free, i, dev), _arg(new_length, "new_length", S, i, dev),
         _arg(tok_off, "tok_off", S + 1, i, dev), _arg(slots, "slots", T, i, dev), _arg(counts, "counts", 3, i, dev),
-        S, max_pages, n_free, T, page, _stream(stream)), "gtattn_cache_slots")
+        S, max_pages, n_free, T, page, stream), "gtattn_cache_slots")
 
 
 def gtattn_cache_append(cache, K, V, slots, T, dtype, stream=None):
     """Stores the keys and values [T, Hkv, D] of T tokens in the cache's
     ``slots`` (int32 [T], as gtattn_cache_slots lists them), in 8 bits."""
-    dev = _call_dev(cache)
-    t, n = _types(dtype)[0], T * cache.Hkv * cache.D
-    _check(load().gtattn_cache_append(cache._ref, _arg(K, "K", n, t, dev), _arg(V, "V", n, t, dev),
-                                      _arg(slots, "slots", T, _i32(), dev), T, dtype, _stream(stream)),
-           "gtattn_cache_append")
+    lib, dev, i, t, _, stream = _call(cache, dtype, stream)
+    n = T * cache.Hkv * cache.D
+    _check(lib.gtattn_cache_append(cache._ref, _arg(K, "K", n, t, dev), _arg(V, "V", n, t, dev),
+                                   _arg(slots, "slots", T, i, dev), T, dtype, stream), "gtattn_cache_append")
 
 
 def gtattn_cache_select(cache, Q, table, length, tok_off, sel, S, T, max_pages, H, n_sel, dtype, stream=None):
     """The pages each row and K/V head reads: its own and the n_sel - 1
     earlier ones whose mean key scores highest; ``sel`` [T, Hkv, n_sel]
     int32, ascending, -1 where there are fewer."""
-    dev, i = _call_dev(cache), _i32()
-    _check(load().gtattn_cache_select(
-        cache._ref, _arg(Q, "Q", T * H * cache.D, _types(dtype)[0], dev), _arg(table, "table", S * max_pages, i, dev),
+    lib, dev, i, t, _, stream = _call(cache, dtype, stream)
+    _check(lib.gtattn_cache_select(
+        cache._ref, _arg(Q, "Q", T * H * cache.D, t, dev), _arg(table, "table", S * max_pages, i, dev),
         _arg(length, "length", S, i, dev), _arg(tok_off, "tok_off", S + 1, i, dev),
-        _arg(sel, "sel", T * cache.Hkv * n_sel, i, dev), S, T, max_pages, H, n_sel, dtype, _stream(stream)),
+        _arg(sel, "sel", T * cache.Hkv * n_sel, i, dev), S, T, max_pages, H, n_sel, dtype, stream),
         "gtattn_cache_select")
 
 
@@ -532,14 +528,13 @@ def gtattn_fwd_cache(cache, Q, table, length, tok_off, out, S, T, max_pages, H, 
     """Attention of T new rows Q [T, H, D] over the cache: all tokens of
     their request up to each row's position, or those in the pages ``sel``
     ([T, Hkv, n_sel] int32) names."""
-    dev, i = _call_dev(cache), _i32()
-    ti, to = _types(dtype)
+    lib, dev, i, ti, to, stream = _call(cache, dtype, stream)
     n = T * H * cache.D
-    _check(load().gtattn_fwd_cache(
+    _check(lib.gtattn_fwd_cache(
         cache._ref, _arg(Q, "Q", n, ti, dev), _arg(table, "table", S * max_pages, i, dev),
         _arg(length, "length", S, i, dev), _arg(tok_off, "tok_off", S + 1, i, dev),
         _arg(sel, "sel", T * cache.Hkv * n_sel, i, dev), _arg(out, "out", n, to, dev), S, T, max_pages, H, n_sel, scale,
-        dtype, _stream(stream)), "gtattn_fwd_cache")
+        dtype, stream), "gtattn_fwd_cache")
 
 
 def sparse_mha(indptr, indices, Q, K, V, scale=None, out=None, plan=None, stream=None):

@@ -217,6 +217,7 @@ __device__ __forceinline__ float power_scale(float amax) {
 }
 
 constexpr int kAppendThreads = 128;
+constexpr int kAppendSpan = 16;
 
 // A block per (token, K/V head, K or V): blocks whose token does not begin a
 // run of consecutive slots in a page leave; the others take the whole run.
@@ -277,12 +278,16 @@ k_append(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const in
 }
 
 
-// The same for D a power of two from 8 on, rows 16-byte aligned: a thread
-// takes 8 features at a time, always the same 8 columns, so the column sums
-// of the mean stay in its registers (they are exact in fp32, in any order).
-// A block looks at `span` consecutive tokens and takes the runs that begin
-// there: one token in a small batch (a run per block), 32 in a large one,
-// where most tokens begin no run.
+// The same for D a power of two from 8 on, rows 16-byte aligned: WPR warps per
+// run (and head, and K or V), a lane 8 features at a time, always the same 8
+// columns, so the column sums of the mean stay in its registers (they are
+// exact in fp32, in any order).  Prompts take a warp per run, which looks at
+// `span` consecutive tokens for runs that begin there: with a block per run
+// its barriers and set-up were most of the 350 instructions a thread spent on
+// 16 elements (17 k fp32 tokens of 8 x 64: APPEND_PROMPT).  Batches too small
+// to fill the SMs with warps take a block per run, four warps on the page's
+// rows (128 single tokens of 8 x 128: 6.4 us, with a warp 10.6: the earlier
+// keys that the mean reads come one after another).
 // Bound by memory: the new rows are read once from DRAM (the second pass over
 // them hits L1), a page's earlier keys are read for its mean.
 __device__ __forceinline__ uint2 eight_e4m3(const float (&x)[8], bool finite) {
@@ -324,28 +329,47 @@ __device__ __forceinline__ uint32_t eight_finite_top(const float (&x)[8]) {
     return t;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kAppendThreads)
+template <typename T, int WPR>
+__global__ void __launch_bounds__(kAppendThreads, 12)
 k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const int* __restrict__ slots, int T_rows,
           int span, int l8) {       // l8 = log2(D / 8)
-    __shared__ uint32_t red[kAppendThreads / 32];
-    __shared__ float cols[kCacheMaxD];
     let_next_start();
     after_previous();
-    const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-    const bool is_v = blockIdx.z != 0;
+    const unsigned full = 0xffffffffu;
+    constexpr int WARPS = kAppendThreads / 32;
+    static_assert(WPR == 1 || WPR == WARPS, "a warp or the block per run");
+    __shared__ uint32_t red[WARPS];
+    __shared__ float cols[WPR > 1 ? WARPS : 1][WPR > 1 ? kCacheMaxD : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int head = WPR > 1 ? blockIdx.y : blockIdx.y * WARPS + warp;            // K and V of each K/V head in turn
+    if (head >= 2 * c.Hkv) return;
+    auto run_max = [&](uint32_t v) {     // over the run's warps
+        v = __reduce_max_sync(full, v);
+        if constexpr (WPR > 1) {
+            __syncthreads();
+            if (lane == 0) red[warp] = v;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) v = max(v, red[w]);
+        }
+        return v;
+    };
+    const int g = head >> 1;
+    const bool is_v = head & 1;
     const int D = c.D, HD = c.Hkv * D, W = 1 << l8;
     const unsigned total = static_cast<unsigned>(c.pages) * c.page;
     const int first = static_cast<int>(min(static_cast<long long>(blockIdx.x) * span, 0x7fffffffll));
-    const int cc = tid & (W - 1), rr = tid >> l8, rows = kAppendThreads >> l8;   // this thread's columns, first row, row step
-    // every warp finds the block's runs: lane i looks at token first + i
+    const int cc = lane & (W - 1), rows = (32 * WPR) >> l8;                       // this lane's columns, the row step
+    const int rr = (WPR > 1 ? warp * 32 + lane : lane) >> l8;                     // and its first row
+    const bool mean = !is_v && c.kmean;
+    // lane i looks at token first + i
     bool begins = false;
     if (lane < span && T_rows - first > lane) {
         const int slot = slots[first + lane];
         begins = static_cast<unsigned>(slot) < total &&
                  ((slot & (c.page - 1)) == 0 || first + lane == 0 || slots[first + lane - 1] != slot - 1);
     }
-    unsigned todo = __ballot_sync(0xffffffffu, begins);
+    unsigned todo = __ballot_sync(full, begins);
     while (todo) {
         const int t = first + __ffs(todo) - 1;
         todo &= todo - 1;
@@ -357,7 +381,7 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
             const int i0 = lane, i1 = lane + 32;
             const bool b0 = !(f + i0 < c.page && T_rows - t > i0 && slots[t + i0] == slot + i0);
             const bool b1 = !(f + i1 < c.page && T_rows - t > i1 && slots[t + i1] == slot + i1);
-            const unsigned m0 = __ballot_sync(0xffffffffu, b0), m1 = __ballot_sync(0xffffffffu, b1);
+            const unsigned m0 = __ballot_sync(full, b0), m1 = __ballot_sync(full, b1);
             n = m0 ? __ffs(m0) - 1 : m1 ? 32 + __ffs(m1) - 1 : 64;
         }
         const T* x = (is_v ? V : K) + static_cast<int64_t>(t) * HD + g * D + cc * 8;
@@ -366,21 +390,13 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
         uint8_t* tile = (is_v ? c.v8 : c.k8) + (ph << c.lp) * D + cc * 8;
         const float old = f > 0 ? *sp : 0.f;
         uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll(WPR > 1 ? 2 : 8)
         for (int i = rr; i < n; i += rows) {
             Eight<T> e;
             e.load(x + static_cast<int64_t>(i) * HD);
             top = max(top, eight_top(e.x));
         }
-        top = __reduce_max_sync(0xffffffffu, top);
-        __syncthreads();                                    // (red and cols of the run before are read)
-        if (lane == 0) red[tid >> 5] = top;
-        const bool mean = !is_v && c.kmean;
-        if (mean)
-            for (int d = tid; d < D; d += kAppendThreads) cols[d] = 0.f;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, red[w]);
+        top = run_max(top);
         const bool finite = top < 0x7f800000u;
         if (!finite) {                                      // once more, of the finite ones
             top = 0;
@@ -389,20 +405,14 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
                 e.load(x + static_cast<int64_t>(i) * HD);
                 top = max(top, eight_finite_top(e.x));
             }
-            top = __reduce_max_sync(0xffffffffu, top);
-            __syncthreads();
-            if (lane == 0) red[tid >> 5] = top;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, red[w]);
+            top = run_max(top);
         }
-        const float amax = __uint_as_float(top);
-        const float now = fmaxf(old, power_scale(amax));
+        const float now = fmaxf(old, power_scale(__uint_as_float(top)));
         float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         const bool grown = f > 0 && now != old;
         if (grown || mean) {
             const float ratio = grown ? old / now : 1.f;
-#pragma unroll 4
+#pragma unroll(WPR > 1 ? 4 : 8)
             for (int i = rr; i < f; i += rows) {
                 uint2* p = reinterpret_cast<uint2*>(tile + i * D);
                 uint2 code = *p;
@@ -420,7 +430,7 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
             }
         }
         const float inv = 1.f / now;                        // (a power of two: exact)
-#pragma unroll 4
+#pragma unroll(WPR > 1 ? 2 : 4)
         for (int i = rr; i < n; i += rows) {
             Eight<T> e;
             e.load(x + static_cast<int64_t>(i) * HD);
@@ -435,18 +445,27 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
                 for (int k = 0; k < 8; ++k) sum[k] += y[k];
             }
         }
-        if (tid == 0) *sp = now;                            // (everyone has read `old`: two barriers ago)
-        if (mean) {
-            // (exact sums: the order of the additions does not matter)
+        if (lane == 0 && (WPR == 1 || warp == 0)) *sp = now;      // (a block's warps have read `old`: run_max)
+        if (mean) {      // (exact sums: the order of the additions does not matter)
+            const float count = static_cast<float>(f + n);
+            float y[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                for (int o = W; o < 32; o <<= 1) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
-                if (lane < W) atomicAdd(&cols[cc * 8 + k], sum[k]);
+                for (int o = W; o < 32; o <<= 1) sum[k] += __shfl_xor_sync(full, sum[k], o);
+                if (WPR > 1 && lane < W) cols[warp][cc * 8 + k] = sum[k];
             }
-            __syncthreads();
-            for (int d = tid; d < D; d += kAppendThreads)
-                c.kmean[ph * D + d] = __float2bfloat16_rn(cols[d] * now / static_cast<float>(f + n));
+            if constexpr (WPR > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] = (cols[0][cc * 8 + k] + cols[1][cc * 8 + k]) + (cols[2][cc * 8 + k] + cols[3][cc * 8 + k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = sum[k] * now / count;
+            if (lane < W && (WPR == 1 || warp == 0))
+                *reinterpret_cast<uint4*>(c.kmean + ph * D + cc * 8) =
+                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
         }
+        __syncwarp();
     }
 }
 
@@ -500,15 +519,18 @@ extern "C" gtattn_status gtattn_cache_append(const gtattn_cache* cache, const vo
     if (eights) {
         int l8 = 0;
         while ((8 << l8) < c.D) ++l8;
-        const int64_t per_sm16 = T * c.Hkv * 2 / (16 * num_sms());
-        const int span = (int)std::min<int64_t>(32, std::max<int64_t>(1, per_sm16));
-        const dim3 grid((unsigned)((T + span - 1) / span), c.Hkv, 2);
+        const int64_t warps = T * c.Hkv * 2;
+        const int span = (int)std::min<int64_t>(kAppendSpan, std::max<int64_t>(1, warps / (32 * num_sms())));
+        constexpr int WARPS = kAppendThreads / 32;
+        const bool block = span == 1;
+        const auto go = [&](auto* one, auto* all, auto* Kp, auto* Vp) {
+            const dim3 grid((unsigned)((T + span - 1) / span), (unsigned)(block ? 2 * c.Hkv : (2 * c.Hkv + WARPS - 1) / WARPS));
+            return launch_after(block ? all : one, grid, kAppendThreads, 0, stream, c, Kp, Vp, slots, (int)T, span, l8);
+        };
+        using B = __nv_bfloat16;
         GT_CUDA(dtype == GTATTN_F32
-                    ? launch_after(k_append8<float>, grid, kAppendThreads, 0, stream, c, static_cast<const float*>(K),
-                                   static_cast<const float*>(V), slots, (int)T, span, l8)
-                    : launch_after(k_append8<__nv_bfloat16>, grid, kAppendThreads, 0, stream, c,
-                                   static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), slots, (int)T,
-                                   span, l8));
+                    ? go(k_append8<float, 1>, k_append8<float, WARPS>, static_cast<const float*>(K), static_cast<const float*>(V))
+                    : go(k_append8<B, 1>, k_append8<B, WARPS>, static_cast<const B*>(K), static_cast<const B*>(V)));
         return GTATTN_OK;
     }
     const dim3 grid((unsigned)T, c.Hkv, 2);

@@ -1,0 +1,8 @@
+// cache_tile128.cu -- the cache attention's tensor-core kernel for heads of 128.
+#include "cache_tile.cuh"
+
+namespace gt {
+gtattn_status cache_tile_128(const CacheAttn& a, gtattn_dtype dtype, int64_t rows, cudaStream_t s) {
+    return launch_tile_d<128>(a, dtype, rows, s);
+}
+}  // namespace gt
