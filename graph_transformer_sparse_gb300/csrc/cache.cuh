@@ -41,6 +41,10 @@ gtattn_status check_cache(const gtattn_cache* c, int need, CacheView* v);
 gtattn_status check_cache_rows(const int32_t* table, const int32_t* length, const int32_t* tok_off, int64_t S,
                                int64_t T, int64_t max_pages, int page, CacheRows* r);
 
+// The error word of the tensor-core cache attention on the current device
+// (gtattn_device_errors).
+cudaError_t cache_tc_errors(int* code, int reset);
+
 // Request of token row t (t < tok_off[S]): the largest s with tok_off[s] <= t.
 __device__ __forceinline__ int request_of(const int* __restrict__ tok_off, int S, int t) {
     int lo = 0, hi = S;   // tok_off[lo] <= t < tok_off[hi]

@@ -122,6 +122,7 @@ extern "C" gtattn_status gtattn_fwd_cache(const gtattn_cache* cache, const void*
     a.q_vec = (reinterpret_cast<uintptr_t>(Q) & 15u) == 0;
     a.o_vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
     const int64_t rows = sel ? a.G : (T * a.G + S - 1) / S;
+    if (a.c.pages > 0 && cache_tc_takes(a, dtype, rows)) return cache_tc(a, dtype, stream);
     if (a.c.pages > 0) switch (a.c.D) {
         case 32: return cache_tile_32(a, dtype, rows, stream);
         case 64: return cache_tile_64(a, dtype, rows, stream);

@@ -23,4 +23,10 @@ gtattn_status cache_tile_32(const CacheAttn& a, gtattn_dtype dtype, int64_t rows
 gtattn_status cache_tile_64(const CacheAttn& a, gtattn_dtype dtype, int64_t rows, cudaStream_t s);
 gtattn_status cache_tile_128(const CacheAttn& a, gtattn_dtype dtype, int64_t rows, cudaStream_t s);
 
+// The same for many rows, on tcgen05 (cache_tc.cu): whether it takes the
+// call, and the call.
+constexpr int kCacheTcMinRows = 64;
+bool cache_tc_takes(const CacheAttn& a, gtattn_dtype dtype, int64_t rows);
+gtattn_status cache_tc(const CacheAttn& a, gtattn_dtype dtype, cudaStream_t s);
+
 }  // namespace gt

@@ -933,7 +933,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cac
 }
 
 // Adds up the parts of the items that were cut.  Items of up to kJoinFew parts
-// go to a block each, a warp a row; of longer ones a block takes one row, its
+// go to a block for every eight rows, a warp a row; of longer ones a block takes one row, its
 // warps every kJoinWarps-th part, added in warp order (one request alone is
 // cut into a part for every few hundred keys; with a warp a row that took
 // 48 us for 76 parts, all of it latency).
@@ -953,10 +953,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) k_cache_join(CacheAttn a, 
         const int tok = a.sel ? 0 : x / a.G, hd = it.g * a.G + (a.sel ? x : x % a.G);
         return (static_cast<int64_t>(it.t0 + tok) * a.H + hd) * D;
     };
-    for (unsigned m = blockIdx.x; m < items; m += gridDim.x) {
-        const Task t = wk.multi[m];
+    constexpr int GROUPS = R / kJoinWarps;
+    for (unsigned long long j = blockIdx.x; j < static_cast<unsigned long long>(items) * GROUPS; j += gridDim.x) {
+        const Task t = wk.multi[j / GROUPS];
         if (t.parts > kJoinFew) continue;
-        for (int row = warp; row < t.it.rows; row += kJoinWarps) {
+        const int row = static_cast<int>(j % GROUPS) * kJoinWarps + warp;
+        if (row < t.it.rows) {
             const int64_t slot = static_cast<int64_t>(t.slot) * R + row;
             float2 ml = make_float2(-INFINITY, 0.f);       // lane i: part i
             if (lane < t.parts) ml = wk.part_ml[slot + lane * R];
@@ -1029,11 +1031,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) k_cache_join(CacheAttn a, 
 }
 
 // ---- host -------------------------------------------------------------------
-template <typename TI, typename TO, int D, int NT, bool SPLITQ, bool SPLITP>
-gtattn_status launch_tile(const CacheAttn& a, cudaStream_t s) {
-    constexpr int R = 8 * NT, smem = tile_smem<D, NT>();
-    auto kernel = k_cache_attn_tile<TI, TO, D, NT, SPLITQ, SPLITP>;
-    const int per_sm = blocks_per_sm(reinterpret_cast<const void*>(kernel), kTileWarps * 32, smem);
+// The plan, a kernel that works through it (tiles of R rows, D features), and
+// the join of what was cut.
+template <typename TO, int D, int R>
+gtattn_status launch_planned(void (*kernel)(CacheAttn, TileWork), int threads, int smem, int tasks_per_block,
+                             const CacheAttn& a, cudaStream_t s) {
+    const int per_sm = blocks_per_sm(reinterpret_cast<const void*>(kernel), threads, smem);
     if (per_sm < 1) return GTATTN_ERR_CUDA;
     const int blocks = num_sms() * per_sm;
     const int64_t rows_all = (int64_t)a.r.T * a.G;
@@ -1044,14 +1047,15 @@ gtattn_status launch_tile(const CacheAttn& a, cudaStream_t s) {
     TileWork wk{};
     if (!cut && items <= blocks) {
         ProfScope ps(GTATTN_KCAT_CACHE, 1, s);
-        GT_CUDA(launch_after(kernel, dim3((unsigned)items), kTileWarps * 32, smem, s, a, wk));
+        GT_CUDA(launch_after(kernel, dim3((unsigned)items), threads, smem, s, a, wk));
         return GTATTN_OK;
     }
-    wk.target = kTasksPerBlock * blocks;
+    wk.target = tasks_per_block * blocks;
     // items of several tasks have more than lc units: at most 2 * units / lc <= 2 * target parts in all
     const size_t slots = cut ? 2 * (size_t)wk.target : 0;
     const size_t n_o = sizeof(float) * slots * R * D, n_ml = sizeof(float2) * slots * R;
-    const size_t n_list = sizeof(Task) * ((size_t)items + slots), n_multi = cut ? sizeof(Task) * (size_t)std::min<int64_t>(items, wk.target) : 0;
+    const size_t n_list = sizeof(Task) * ((size_t)items + slots);
+    const size_t n_multi = cut ? sizeof(Task) * (size_t)std::min<int64_t>(items, wk.target) : 0;
     const size_t n_pre = a.sel || a.r.S <= kPlanHeld ? 0 : 3 * sizeof(int) * (size_t)a.r.S;
     void* ws = nullptr;
     GT_TRY(pool_alloc(&ws, n_o + n_ml + n_list + sizeof(TilePlan) + n_multi + n_pre, s));
@@ -1069,14 +1073,19 @@ gtattn_status launch_tile(const CacheAttn& a, cudaStream_t s) {
         e = launch_after(k_cache_plan, dim3((unsigned)std::min<int64_t>(num_sms(), (list + 2 * kPlanThreads - 1) / (2 * kPlanThreads))),
                          kPlanThreads, 0, s, a, wk, R);
         if (e == cudaSuccess)
-            e = launch_after(kernel, dim3((unsigned)(cut ? blocks : std::min<int64_t>(blocks, items))), kTileWarps * 32, smem, s, a, wk);
-        if (cut && e == cudaSuccess) {
+            e = launch_after(kernel, dim3((unsigned)(cut ? blocks : std::min<int64_t>(blocks, items))), threads, smem, s, a, wk);
+        if (cut && e == cudaSuccess)
             e = launch_after(k_cache_join<TO, D, R>, dim3((unsigned)std::min<int64_t>(items * R, num_sms() * 4)), kJoinWarps * 32, 0,
                              s, a, wk);
-        }
     }
     pool_free(ws, s);
     return e == cudaSuccess ? GTATTN_OK : cuda_status(e);
+}
+
+template <typename TI, typename TO, int D, int NT, bool SPLITQ, bool SPLITP>
+gtattn_status launch_tile(const CacheAttn& a, cudaStream_t s) {
+    return launch_planned<TO, D, 8 * NT>(k_cache_attn_tile<TI, TO, D, NT, SPLITQ, SPLITP>, kTileWarps * 32, tile_smem<D, NT>(),
+                                         kTasksPerBlock, a, s);
 }
 
 template <int D, int NT> gtattn_status launch_tile_n(const CacheAttn& a, gtattn_dtype dtype, cudaStream_t s) {

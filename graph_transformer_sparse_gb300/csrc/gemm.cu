@@ -23,6 +23,7 @@
 // Other shapes and fp32 operands take a CUDA-core kernel (64 x 64 tiles,
 // 4 x 4 outputs a thread, fp32 FMAs in ascending k).
 #include "gemm.cuh"
+#include "cache.cuh"
 #include "tc.cuh"
 
 #include <algorithm>
@@ -513,5 +514,8 @@ extern "C" gtattn_status gtattn_device_errors(int* code, int reset) {
         const int zero = 0;
         GT_CUDA(cudaMemcpyToSymbol(g_gemm_errors, &zero, sizeof(int)));
     }
+    int cache = 0;
+    GT_CUDA(cache_tc_errors(&cache, reset));
+    *code |= cache;
     return GTATTN_OK;
 }

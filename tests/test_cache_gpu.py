@@ -494,6 +494,51 @@ def test_attend_extremes(D, dtype):
     check_attend(st, f64(tQ), tQ, off, H, dtype, 0.0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "bf16_out_f32"])
+@pytest.mark.parametrize("H,Hkv,D,page", [(4, 4, 64, 16), (4, 2, 128, 32), (6, 2, 64, 64), (3, 1, 128, 16)])
+def test_attend_many_rows(dtype, H, Hkv, D, page):
+    # tiles of 128 rows: lengths around the tiles' and pages' ends, requests of a few rows and of none among them
+    rng = np.random.default_rng(H + D + page)
+    adds = [257, 1, 0, 128, 300, 40]
+    st = Store(rng, [257, 500, 3, 128, 700, 129], Hkv, D, page)
+    off = offsets(adds)
+    tQ, Q = typed(rng, (off[-1] + 5, H, D), dtype)
+    got = check_attend(st, Q, tQ, off, H, dtype, D ** -0.5)
+    cache = st.cache()
+    for _ in range(3):
+        again = run_attend(st, tQ, off, H, dtype, D ** -0.5, cache=cache)
+        assert np.array_equal(f64(again), got)
+    assert gt.gtattn_device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "bf16_out_f32"])
+def test_attend_many_rows_odd_values(D, dtype):
+    # NaN in keys and values of tokens that some rows do not see, scales far apart, bad pages, unlike queries
+    rng = np.random.default_rng(D)
+    H, Hkv, page = 4, 2, 16
+    for which in ("k8", "v8"):
+        st = Store(rng, [400, 330], Hkv, D, page)
+        off = offsets([200, 150])
+        for at, g, d in ((250, 1, 3), (250, 1, D - 1), (399, 0, 0), (290, 0, D // 2)):
+            getattr(st, which)[st.table[0, at // page], g, at % page, d] = 0x7f
+        st.vs[st.table[1]] = 2.0 ** rng.integers(-30, 20, (len(st.table[1]), Hkv))
+        st.ks[st.table[1]] = 2.0 ** rng.integers(-20, -4, (len(st.table[1]), Hkv))
+        st.table[1, 3], st.table[1, 8] = -1, st.k8.shape[0]
+        tQ, Q = typed(rng, (350, H, D), dtype)
+        tQ[210] *= 64
+        tQ[211] *= 2.0 ** -30
+        tQ[212] = 0
+        got = check_attend(st, f64(tQ), tQ, off, H, dtype, D ** -0.5)
+        seen = np.isnan(got[:200]).any(2)
+        assert not seen[:50].any() and seen[50:, 2:].all() and not seen[:90, :2].any() and seen[90:, :2].all()
+        assert not np.isnan(got[200:]).any()
+    # rows of requests that hold fewer tokens than they have rows
+    tQ, Q = typed(rng, (350, H, D), dtype)
+    st = Store(rng, [400, 330], Hkv, D, page)
+    check_attend(st, Q, tQ, off, H, dtype, -0.3, lengths=[120, -9])
+
+
 @pytest.mark.parametrize("D", [64, 40])
 def test_attend_bad_pages_and_lengths(D):
     rng = np.random.default_rng(11)
