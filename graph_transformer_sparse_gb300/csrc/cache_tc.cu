@@ -6,9 +6,9 @@
 // codes by 16-byte loads, converted to fp16 (exact) and stored in the
 // 128-byte-swizzled layout that the products read.  Warps 0-3 are the rows, a
 // thread each (= its lane of tensor memory): S_j = Q K_j^T comes out of tensor
-// memory in pieces of 32 columns, twice -- for the maximum, and for the weights
-// -- and the weights go back over it as fp16 (with a second fp16 for the rest
-// where the output is fp32).  Then one thread issues O += P_j V_j and S_(j+1),
+// memory in pieces of 32 columns and goes back as weights in fp16 (with a
+// second fp16 for the rest where the output is fp32), under the maximum so far;
+// where that is not known yet or has become too small S_j is read twice.  Then one thread issues O += P_j V_j and S_(j+1),
 // and everybody meets at its end; meanwhile warps 4-7 have stored tile j + 1.
 // The other block of the SM works while this one waits.  Scales, the running
 // maximum's slack and the cut of the work are those of cache_tile.cuh, and so
@@ -29,7 +29,7 @@ __device__ int g_cache_errors;      // 1: a bounded wait gave up
 
 constexpr int kTcThreads = 256;
 constexpr int kTcRows = 128;
-constexpr int kTcTasks = 3;         // tasks aimed at for each resident block
+constexpr int kTcTasks = 2;         // tasks aimed at for each resident block
 constexpr uint32_t kTcCols = 256;   // tensor memory of a block: S and P, then O
 constexpr uint32_t kTcColO = 128;
 
@@ -37,6 +37,11 @@ template <int D> struct TcCfg {
     static constexpr int KT = D == 64 ? 128 : 64;             // keys a tile
     static constexpr int GR = KT / 16;                        // groups of 16 keys (one page, one scale)
     static constexpr int QB = kTcRows * D * 2, KB = KT * D * 2;
+    // columns of the weights: beside S where they fit (S can then be read again), else over it
+    static constexpr bool apart(bool split) { return D == 128 || !split; }
+    static constexpr uint32_t col_p(bool split) { return !apart(split) ? 0u : D == 128 ? 64u : 192u; }
+    static constexpr uint32_t col_step(bool split) { return apart(split) ? 16u : 32u; }     // 32 keys
+    static constexpr uint32_t col_rest(bool split) { return apart(split) ? 32u : 16u; }     // their rests
     static constexpr int SMEM = QB + 4 * KB + 1024;           // Q, two stages of K and V, alignment
 };
 
@@ -66,11 +71,18 @@ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// What a stage's 16-key groups are.
+// A 16-key group of a tile: page (below 0: none), valid keys, scales.
 struct Group {
-    int pid, cnt;        // page (below 0: none), valid keys
+    int pid, cnt;
     float ks, vs;
 };
+// What the rows need of it: the keys' scale, log2 of the values' and its inverse.
+struct alignas(16) GroupFacts {
+    int cnt;
+    float ks, lv, iv;
+};
+constexpr float kTcBase = 4.f;          // weights are 2^(a - M + 4) ...
+constexpr float kTcSumLimit = 32768.f;  // ... and a tile's add up to this at most, or M moves
 
 template <typename TO, int D, bool SPLITP>
 __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, TileWork wk) {
@@ -84,7 +96,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, Ti
     auto sV = [&](int b) { return smem + C::QB + b * 2 * C::KB + C::KB; };
     __shared__ Task sm_task[2];
     __shared__ int sm_more[2];
-    __shared__ Group sm_group[2][GR];
+    __shared__ GroupFacts sm_group[2][GR];
+    __shared__ int sm_page[2][GR];
     // per tile (j mod 3): keys whose value holds a NaN, where some row does not see them; written while tile
     // j - 1 is worked on, read with tile j, cleared with tile j + 1
     __shared__ uint32_t sm_nan[3][4];
@@ -188,7 +201,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, Ti
         auto store = [&](const Group& h, int j) {
             const int b = j & 1;
             const bool diagonal = key_b + (j + 1) * KT - 1 > min_pos;
-            if (lane < GPW) sm_group[b][lw * GPW + lane] = h;
+            if (lane < GPW) {
+                const uint32_t e = __float_as_uint(h.vs) & 0x7f800000u;
+                sm_page[b][lw * GPW + lane] = h.pid;
+                sm_group[b][lw * GPW + lane] =
+                    GroupFacts{h.cnt, h.ks, static_cast<float>(static_cast<int>(e >> 23) - 127), __uint_as_float((254u << 23) - e)};
+            }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int ch = x * 32 + lane, row = ch / (D / 16), col = ch % (D / 16), key = lw * KPW + row;
@@ -209,10 +227,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, Ti
                 put8(sV(b), key, 2 * col + 1, vr[x].z, vr[x].w);
             }
         };
-        Group g0{}, g1{};                 // groups of the tile being fetched, and of the next
+        Group g0{}, g1{}, g2{};           // groups of the tile being fetched, and of the two after it
         if (!rows_side) {
             g0 = look(0);
             g1 = look(1);
+            g2 = look(2);
             if (T > 0) {
                 fetch(g0, 0);
                 store(g0, 0);
@@ -285,27 +304,54 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, Ti
             if (!rows_side) {
                 // tile j + 1: under way before S_j is there, stored after it (O += P_(j-1) V_(j-1) has then read its stage)
                 g0 = g1;
+                g1 = g2;
                 if (j + 1 < T) fetch(g0, j + 1);
-                g1 = look(j + 2);
+                g2 = look(j + 3);
                 ok = wait_mma();
                 if (j + 1 < T) store(g0, j + 1);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             } else {
                 ok = wait_mma();
-                const uint32_t tS = tmem + lane_base;
+                const uint32_t tS = tmem + lane_base, tP = tS + C::col_p(SPLITP);
                 const int key0 = key_b + j * KT;
-                float top = -INFINITY;
+                const int ahead = pos - key0;          // the row sees the tile's keys 0 .. ahead
+                // a = logit + log2(vscale) of columns 32 x + 16 q .. + 15, -inf where the row does not see the key
+                auto logits = [&](const uint32_t* s, const GroupFacts& g, int first, float* v) {
+                    const float cs = cq * g.ks;
 #pragma unroll
-                for (int pass = 0; pass < 2; ++pass) {
-                    if (pass == 1) {
-                        // the running maximum moves when a weight would pass 2^15
-                        const bool move = top > M + kPSlack;
-                        if (__any_sync(full, move)) {
+                    for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(s[k]), cs, g.lv);
+                    const int see = min(g.cnt, ahead - first + 1);
+                    if (see < 16) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (k >= see) v[k] = -INFINITY;
+                    }
+                };
+                // The maximum is looked for in a task's first tile, and where a tile's weights grow too large
+                // under the one so far (or, where the weights take S's place, before it is known: always).
+                bool look_top = j == 0 || !C::apart(SPLITP);
+                for (;;) {
+                    if (look_top) {
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int x = 0; x < KT / 32; ++x) {
+                            uint32_t s[32];
+                            tmem_ld32(tS + 32 * x, s);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                float v[16];
+                                logits(s + 16 * q, sm_group[b][2 * x + q], 32 * x + 16 * q, v);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) top = fmaxf(top, v[k]);
+                            }
+                        }
+                        if (__any_sync(full, top > M + (C::apart(SPLITP) ? 0.f : kPSlack))) {
                             const float t = fmaxf(top, M), f = M == t ? 1.f : ex2(M - t);
                             M = t;
                             l *= f;
                             if (j > 0) {
-#pragma unroll
+#pragma unroll 1
                                 for (int x = 0; x < D / 32; ++x) {
                                     uint32_t o[32];
                                     tmem_ld32(tmem + lane_base + kTcColO + 32 * x, o);
@@ -317,8 +363,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, Ti
                             }
                         }
                     }
-                    const float mu = (M == -INFINITY ? 0.f : M) - kPBase;
-#pragma unroll
+                    const float mu = (M == -INFINITY ? 0.f : M) - kTcBase;
+                    float sum = 0.f, scaled = 0.f;
+#pragma unroll 1
                     for (int x = 0; x < KT / 32; ++x) {
                         uint32_t s[32];
                         tmem_ld32(tS + 32 * x, s);
@@ -326,44 +373,39 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, Ti
                         uint32_t p[SPLITP ? 32 : 16];
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const Group g = sm_group[b][2 * x + q];
-                            const float cs = cq * g.ks;
-                            const float lv = static_cast<float>(static_cast<int>((__float_as_uint(g.vs) >> 23) & 0xff) - 127);
-                            // keys of the group that the row sees
-                            const long long left = static_cast<long long>(pos) + 1 - (key0 + 32 * x + 16 * q);
-                            const int see = static_cast<int>(min(static_cast<long long>(g.cnt), left));
+                            const GroupFacts g = sm_group[b][2 * x + q];
                             float v[16];
+                            logits(s + 16 * q, g, 32 * x + 16 * q, v);
+                            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(s[16 * q + k]), cs, lv);
-                            if (see < 16) {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    if (k >= see) v[k] = -INFINITY;
+                            for (int k = 0; k < 16; k += 2) {
+                                v[k] = ex2(v[k] - mu);
+                                v[k + 1] = ex2(v[k + 1] - mu);
+                                s0 += v[k];
+                                s1 += v[k + 1];
+                                const uint32_t h = pack_f16x2(v[k], v[k + 1]);
+                                p[8 * q + k / 2] = h;
+                                if constexpr (SPLITP) p[16 + 8 * q + k / 2] = rest_f16x2(v[k], v[k + 1], h);
                             }
-                            if (pass == 0) {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) top = fmaxf(top, v[k]);
-                            } else {
-                                float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-                                for (int k = 0; k < 16; k += 2) {
-                                    v[k] = ex2(v[k] - mu);
-                                    v[k + 1] = ex2(v[k + 1] - mu);
-                                    sum0 += v[k];
-                                    sum1 += v[k + 1];
-                                    const uint32_t h = pack_f16x2(v[k], v[k + 1]);
-                                    p[8 * q + k / 2] = h;
-                                    if constexpr (SPLITP) p[16 + 8 * q + k / 2] = rest_f16x2(v[k], v[k + 1], h);
-                                }
-                                l = fmaf(sum0 + sum1, __uint_as_float((254u << 23) - (__float_as_uint(g.vs) & 0x7f800000u)), l);
-                            }
+                            s0 += s1;
+                            sum += s0;
+                            scaled = fmaf(s0, g.iv, scaled);
                         }
-                        if (pass == 1) {
-                            // over the columns just read: weights 32 x .. in columns 32 x .. + 15, their rests behind them
-                            if constexpr (SPLITP) tmem_st32(tS + 32 * x, p);
-                            else tmem_st16(tS + 32 * x, p);
+                        if constexpr (!SPLITP) {
+                            tmem_st16(tP + C::col_step(false) * x, p);
+                        } else if constexpr (C::apart(true)) {
+                            tmem_st16(tP + C::col_step(true) * x, p);
+                            tmem_st16(tP + C::col_step(true) * x + C::col_rest(true), p + 16);
+                        } else {
+                            tmem_st32(tP + C::col_step(true) * x, p);
                         }
                     }
+                    const bool over = !look_top && !(sum <= kTcSumLimit);      // (a NaN: looked for once)
+                    if (!__any_sync(full, over)) {
+                        l += scaled;
+                        break;
+                    }
+                    look_top = true;
                 }
                 tmem_st_wait();
                 if (tid < 4) sm_nan[(j + 2) % 3][tid] = 0;
@@ -371,7 +413,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, Ti
                 if (nan[0] | nan[1] | nan[2] | nan[3]) {
                     for (int k = 0; k < KT; ++k) {
                         if (!((nan[k >> 5] >> (k & 31)) & 1u) || !valid || key0 + k > pos) continue;
-                        const int64_t ph = static_cast<int64_t>(sm_group[b][k >> 4].pid) * c.Hkv + it.g;
+                        const int64_t ph = static_cast<int64_t>(sm_page[b][k >> 4]) * c.Hkv + it.g;
                         const uint8_t* v = c.v8 + ((ph << c.lp) + ((key0 + k) & (c.page - 1))) * D;
 #pragma unroll
                         for (int d = 0; d < D; ++d)
@@ -387,9 +429,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, Ti
                 const uint64_t dV = smem_desc_sw128(su32(sV(b)), SUB, 1024);
 #pragma unroll
                 for (int k = 0; k < KT / 16; ++k) {           // 16 keys: 8 columns of P, 16 rows of V
-                    const uint32_t pa = tmem + 32 * (k >> 1) + 8 * (k & 1);
+                    const uint32_t pa = tmem + C::col_p(SPLITP) + C::col_step(SPLITP) * (k >> 1) + 8 * (k & 1);
                     mma_ts(tmem + kTcColO, pa, dV + k * 128, idO, j > 0 || k > 0);
-                    if constexpr (SPLITP) mma_ts(tmem + kTcColO, pa + 16, dV + k * 128, idO, 1u);
+                    if constexpr (SPLITP) mma_ts(tmem + kTcColO, pa + C::col_rest(SPLITP), dV + k * 128, idO, 1u);
                 }
                 if (j + 1 < T) issue_s(b ^ 1);
                 commit_one(&bar);
@@ -454,11 +496,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_cache_attn_tc(CacheAttn a, Ti
     }
 }
 
+// (two blocks an SM: registers and shared memory are cut for that; the occupancy query says one of a kernel
+// that allocates tensor memory, though two take half of it each)
 template <int D> gtattn_status launch_tc(const CacheAttn& a, gtattn_dtype dtype, cudaStream_t s) {
     using B = __nv_bfloat16;
     if (dtype == GTATTN_BF16)
-        return launch_planned<B, D, kTcRows>(k_cache_attn_tc<B, D, false>, kTcThreads, TcCfg<D>::SMEM, kTcTasks, a, s);
-    return launch_planned<float, D, kTcRows>(k_cache_attn_tc<float, D, true>, kTcThreads, TcCfg<D>::SMEM, kTcTasks, a, s);
+        return launch_planned<B, D, kTcRows>(k_cache_attn_tc<B, D, false>, kTcThreads, TcCfg<D>::SMEM, kTcTasks, a, s, 2);
+    return launch_planned<float, D, kTcRows>(k_cache_attn_tc<float, D, true>, kTcThreads, TcCfg<D>::SMEM, kTcTasks, a, s, 2);
 }
 
 }  // namespace

@@ -1032,12 +1032,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) k_cache_join(CacheAttn a, 
 
 // ---- host -------------------------------------------------------------------
 // The plan, a kernel that works through it (tiles of R rows, D features), and
-// the join of what was cut.
+// the join of what was cut.  resident: blocks an SM, where the occupancy that
+// CUDA reports is not it.
 template <typename TO, int D, int R>
 gtattn_status launch_planned(void (*kernel)(CacheAttn, TileWork), int threads, int smem, int tasks_per_block,
-                             const CacheAttn& a, cudaStream_t s) {
-    const int per_sm = blocks_per_sm(reinterpret_cast<const void*>(kernel), threads, smem);
+                             const CacheAttn& a, cudaStream_t s, int resident = 0) {
+    int per_sm = blocks_per_sm(reinterpret_cast<const void*>(kernel), threads, smem);
     if (per_sm < 1) return GTATTN_ERR_CUDA;
+    if (resident) per_sm = resident;
     const int blocks = num_sms() * per_sm;
     const int64_t rows_all = (int64_t)a.r.T * a.G;
     const int64_t keys = a.sel ? (int64_t)a.n_sel * a.c.page : (int64_t)a.r.max_pages * a.c.page;
