@@ -490,6 +490,8 @@ extern "C" gtattn_status gtattn_cache_slots(const int32_t* length, const int32_t
                           (const void*)new_length, (const void*)tok_off, (const void*)slots, (const void*)counts})
         al |= reinterpret_cast<uintptr_t>(p);
     if (al & 3u) return GTATTN_ERR_INVALID_ARG;
+    // every block reads the lengths before its own requests again: they must not change meanwhile
+    if (S > 0 && new_length < length + S && length < new_length + S) return GTATTN_ERR_INVALID_ARG;
     const SlotsArgs a{length, add, table, free_pages, new_length, tok_off, slots, counts,
                       (int)S, (int)max_pages, (int)n_free, (int)T, page};
     ProfScope ps(GTATTN_KCAT_CACHE, 1, stream);

@@ -46,8 +46,18 @@ gtattn_status check_cache_rows(const int32_t* table, const int32_t* length, cons
 cudaError_t cache_tc_errors(int* code, int reset);
 
 // Request of token row t (t < tok_off[S]): the largest s with tok_off[s] <= t.
+// Looked for at s = t first: with a token for each request it is there, and
+// the search's dependent loads are saved.
+__device__ __forceinline__ bool request_guess(const int* __restrict__ tok_off, int S, int t, int* s) {
+    *s = min(t, S - 1);
+    const int a = __ldg(tok_off + *s), b = __ldg(tok_off + *s + 1);
+    return a <= t && t < b;
+}
 __device__ __forceinline__ int request_of(const int* __restrict__ tok_off, int S, int t) {
-    int lo = 0, hi = S;   // tok_off[lo] <= t < tok_off[hi]
+    int lo;
+    if (request_guess(tok_off, S, t, &lo)) return lo;
+    lo = 0;
+    int hi = S;   // tok_off[lo] <= t < tok_off[hi]
     while (hi - lo > 1) {
         const int m = (lo + hi) >> 1;
         if (__ldg(tok_off + m) <= t) lo = m;
@@ -55,14 +65,16 @@ __device__ __forceinline__ int request_of(const int* __restrict__ tok_off, int S
     }
     return lo;
 }
-
 // The same by a whole warp, 32 places a look.
 __device__ __forceinline__ int request_of_warp(const int* __restrict__ tok_off, int S, int t, int lane) {
-    int lo = 0, n = S;
+    int lo;
+    if (request_guess(tok_off, S, t, &lo)) return lo;
+    lo = 0;
+    int n = S;
     while (n > 1) {
         const int step = (n + 31) / 32;
         const bool le = lane * step < n && __ldg(tok_off + lo + lane * step) <= t;
-        const int i = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+        const int i = max(__popc(__ballot_sync(0xffffffffu, le)) - 1, 0);
         lo += i * step;
         n = min(step, n - i * step);
     }

@@ -44,8 +44,9 @@ struct SelItem {
 __device__ __forceinline__ bool sel_item(const SelArgs& a, int64_t item, SelItem* it) {
     it->t = a.t0 + static_cast<int>(item / a.c.Hkv);
     it->g = static_cast<int>(item % a.c.Hkv);
-    if (it->t >= __ldg(a.r.tok_off + a.r.S)) return false;
+    const int end = __ldg(a.r.tok_off + a.r.S);
     it->s = request_of_warp(a.r.tok_off, a.r.S, it->t, threadIdx.x & 31);
+    if (it->t >= end) return false;
     it->pos = position_of(a.r, a.c.page, it->s, it->t);
     it->own = it->pos < 0 ? -1 : it->pos >> a.c.lp;
     return true;

@@ -163,7 +163,7 @@ struct TilePlan {
     unsigned tasks;
     unsigned multi;      // items of several tasks
     int most;            // the most tasks of one item
-    unsigned next;       // tasks claimed beyond the blocks' first
+    unsigned next;       // tasks claimed beyond the blocks' own (two each, one in cache_tc.cu)
     int pad[3];
 };
 // A task, units [j0, j1) of an item, as the plan lists it.
@@ -257,8 +257,7 @@ struct Share {
 };
 __device__ __forceinline__ Share share_of(const CacheAttn& a, int s, int R) {
     Share h;
-    const int t0 = __ldg(a.r.tok_off + s);
-    h.n = __ldg(a.r.tok_off + s + 1) - t0;
+    h.n = min(__ldg(a.r.tok_off + s + 1), a.r.T) - __ldg(a.r.tok_off + s);       // (rows past T do not exist)
     const long long cap = static_cast<long long>(a.r.max_pages) * a.c.page;
     h.len = static_cast<int>(min(static_cast<long long>(max(__ldg(a.r.length + s), 0)), cap));
     h.tiles = h.n > 0 ? static_cast<int>((static_cast<long long>(h.n) * a.G + R - 1) / R) : 0;
@@ -275,7 +274,7 @@ __device__ __forceinline__ Item item_full(const CacheAttn& a, int R, int s, unsi
     it.t0 = __ldg(a.r.tok_off + s);
     it.q0 = static_cast<int>(k % h.tiles) * R;
     it.rows = min(R, h.n * a.G - it.q0);
-    const long long p0 = static_cast<long long>(__ldg(a.r.length + s)) - h.n;
+    const long long p0 = static_cast<long long>(__ldg(a.r.length + s)) - (__ldg(a.r.tok_off + s + 1) - it.t0);
     const long long cap = static_cast<long long>(a.r.max_pages) * a.c.page - 1;
     it.pos0 = static_cast<int>(max(p0, -(1ll << 31)));
     // up to the tile's last token, its position capped as position_of caps it
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheAttn a, TileWo
     const bool lead = blockIdx.x == 0 && tid == 0;
     if (a.sel) {
         const int units = sel_units(a);
-        const long long items = static_cast<long long>(__ldg(a.r.tok_off + S)) * a.c.Hkv * ((a.G + R - 1) / R);
+        const long long items = static_cast<long long>(min(__ldg(a.r.tok_off + S), a.r.T)) * a.c.Hkv * ((a.G + R - 1) / R);
         const int lc = static_cast<int>(max((items * units + wk.target - 1) / wk.target, 1ll));
         const int nch = (units + lc - 1) / lc;
         if (lead) *wk.plan = TilePlan{lc, static_cast<unsigned>(items * nch), nch > 1 ? static_cast<unsigned>(items) : 0u, nch, 0u};
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheAttn a, TileWo
 // The item that block b takes when there is no plan (at most one each, of one unit): the warp walks the requests.
 __device__ __forceinline__ bool task_plain(const CacheAttn& a, int R, unsigned b, int lane, Task* t) {
     if (a.sel) {
-        if (b >= static_cast<long long>(__ldg(a.r.tok_off + a.r.S)) * a.c.Hkv * ((a.G + R - 1) / R)) return false;
+        if (b >= static_cast<long long>(min(__ldg(a.r.tok_off + a.r.S), a.r.T)) * a.c.Hkv * ((a.G + R - 1) / R)) return false;
         t->it = item_sel(a, R, b);
     } else {
         long long before = 0;
@@ -504,10 +503,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cac
     after_previous();
 
     const unsigned tasks = wk.plan ? wk.plan->tasks : 0;
-    // Task i of this block (0: by its place in the grid, others claimed) goes to sm_task by way of warp 0's
+    // Task i of this block (0 and 1: by its place in the grid, others claimed) goes to sm_task by way of warp 0's
     // registers: claimed when the block begins task i - 2, read a few steps later, put down at that task's end.
     // (Fetched in one go, the three dependent accesses held warp 0, and with it the block, up for 2 us a task.)
-    auto claim = [&]() { return lane == 0 && wk.plan ? gridDim.x + atomicAdd(&wk.plan->next, 1u) : 0u; };
+    auto claim = [&]() { return lane == 0 && wk.plan ? 2 * gridDim.x + atomicAdd(&wk.plan->next, 1u) : 0u; };
     auto task_word = [&](unsigned x) {       // lane i: word i of task x
         return lane < kTaskWords && x < tasks ? reinterpret_cast<const int*>(wk.list + x)[lane] : 0;
     };
@@ -517,9 +516,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cac
     };
     if (warp == 0) {
         if (wk.plan) {
-            const unsigned x1 = __shfl_sync(full, claim(), 0);
-            put(0, blockIdx.x, task_word(blockIdx.x));
-            put(1, x1, task_word(x1));
+            const unsigned x1 = gridDim.x + blockIdx.x;
+            const int w0 = task_word(blockIdx.x), w1 = task_word(x1);
+            put(0, blockIdx.x, w0);
+            put(1, x1, w1);
         } else {
             Task t{};
             const bool more = task_plain(a, R, blockIdx.x, lane, &t);

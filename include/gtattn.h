@@ -424,7 +424,7 @@ gtattn_status gtattn_fwd_proj(const int32_t* indptr, const int32_t* indices, con
 /*
  * gtattn_device_errors -- error codes recorded on the current device by
  * kernels that have no plan to report into (the tensor-core projections of
- * gtattn_fwd_proj): the bitwise OR since the last reset, 1 = a bounded wait
+ * gtattn_fwd_proj, gtattn_fwd_cache on many rows): the bitwise OR since the last reset, 1 = a bounded wait
  * gave up (its results are not valid).  Synchronises the device; with
  * `reset`, clears the record.
  */
@@ -464,7 +464,8 @@ gtattn_status gtattn_csr_validate(const int32_t* indptr, const int32_t* indices,
  *   k8, v8:  e4m3 codes [pages, Hkv, page, D]; the value is code * scale.
  *   kscale, vscale: fp32 [pages, Hkv], powers of two, so that a page whose
  *            scale grows is rescaled without rounding (but for codes that
- *            become subnormal).
+ *            become subnormal); vscale of the pages that one row reads within
+ *            2^100 of each other.
  *   kmean:   bf16 [pages, Hkv, D], the mean of the page's stored keys (as
  *            stored, rounded once): what gtattn_cache_select scores.  May be
  *            NULL where no call selects.
@@ -481,6 +482,7 @@ gtattn_status gtattn_csr_validate(const int32_t* indptr, const int32_t* indices,
  * their results are left as they were.  Page ids outside [0, pages) hold
  * nothing: attention skips them and their score is 0; a length beyond the
  * table counts as the table's end.  The contents of tok_off are not checked.
+ * Request s's rows past T do not exist.
  * S, T < 2^31 - 1, max_pages * page < 2^31.  Q and out are [T, H, D], H a
  * multiple of Hkv and at most 1024: query head h reads K/V head h / (H / Hkv).
  * All calls are asynchronous on `stream`; temporaries come from the
@@ -503,7 +505,7 @@ typedef struct {
  *   table:      [S, max_pages]; entries of newly taken pages are written, the
  *               others are read only.
  *   free_pages: int32 [n_free]; taken from the front, in request order.
- *   new_length: int32 [S], length + add (must not overlap length).
+ *   new_length: int32 [S], length + add (overlapping length: INVALID_ARG).
  *   tok_off:    int32 [S+1], the rows of each request (see above).
  *   slots:      int32 [T], rows in order; -1 from tok_off[S] on.
  *   counts:     int32 [3]: pages taken, rows (tok_off[S]), requests refused.
@@ -569,7 +571,12 @@ gtattn_status gtattn_cache_select(const gtattn_cache* cache, const void* Q, cons
  *        are skipped, a page listed twice weighs twice.
  * A row without tokens to read gives zeros.  Accumulation is fp32 and every
  * row's result reads only the tokens it may see (a NaN in a later token or
- * an unused place reaches no earlier row).
+ * an unused place reaches no earlier row).  Queries are held to 2^-40 of
+ * their row's largest; the softmax weights in 11 bits where out is bf16, in 21
+ * or more where it is fp32.  D = 32, 64 and 128 run on the tensor cores
+ * (tcgen05 from 64 rows a request and K/V head on, bf16 queries, D 64 or 128,
+ * no sel), other widths on the CUDA cores; a bounded device wait that gives up
+ * is reported by gtattn_device_errors.
  * Errors: INVALID_ARG, UNSUPPORTED (T * H >= 2^31), NO_MEMORY, CUDA.
  */
 gtattn_status gtattn_fwd_cache(const gtattn_cache* cache, const void* Q, const int32_t* table, const int32_t* length,

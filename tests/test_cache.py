@@ -27,8 +27,8 @@ BAD_CACHES = [dict(page=8), dict(page=48), dict(page=128), dict(page=0), dict(pa
 
 def test_slots_refusals(lib):
     f = lib.gtattn_cache_slots   # length add table free new_length tok_off slots counts S max_pages n_free T page stream
-    ok = [16, 16, 16, 16, 16, 16, 16, 16, 4, 4, 4, 4, 16, None]
-    for at, bad in [(0, None), (1, None), (2, None), (3, None), (4, None), (5, None), (6, None), (7, None), (0, 18), (2, 17),
+    ok = [16, 16, 16, 16, 64, 16, 16, 16, 4, 4, 4, 4, 16, None]
+    for at, bad in [(4, 16), (4, 28), (4, 4), (0, None), (1, None), (2, None), (3, None), (4, None), (5, None), (6, None), (7, None), (0, 18), (2, 17),
                     (3, 18), (4, 18), (5, 18), (6, 18), (7, 18), (8, -1), (9, -1), (10, -1), (11, -1), (8, 1 << 31),
                     (10, 1 << 31), (11, 1 << 31), (9, 1 << 27), (9, 1 << 62), (12, 0), (12, 8), (12, 128), (12, -16)]:
         a = list(ok)

@@ -556,6 +556,29 @@ def test_attend_bad_pages_and_lengths(D):
     check_attend(st, Q, tQ, off, H, "f32", 0.2, lengths=[100, 2 ** 31 - 1, 64, 64, 65])
 
 
+@pytest.mark.parametrize("H,D,T", [(4, 64, 3), (4, 64, 300), (4, 128, 200), (4, 40, 5)])
+def test_attend_rows_past_the_batch_and_empty_tables(H, D, T):
+    # offsets that pass T: only rows below T are written; a table without pages, a cache without pages: zeros
+    rng = np.random.default_rng(17)
+    st = Store(rng, [400, 60], 2, D, 16)
+    off = offsets([T, 9])
+    tQ, Q = typed(rng, (T, H, D), "bf16")
+    flat = torch.full((T + 20, H, D), 77.0, dtype=torch.bfloat16, device="cuda")
+    gt.gtattn_fwd_cache(st.cache(), tQ, ints(st.table), ints(st.lengths), ints(off), flat[:T], 2, T, st.max_pages, H, 0.1,
+                        gt.GTATTN_BF16)
+    torch.cuda.synchronize()
+    assert (flat[T:] == 77).all()
+    assert torch.equal(flat[:T], run_attend(st, tQ, offsets([T, 0]), H, "bf16", 0.1))
+    out = torch.full((T, H, D), 77.0, dtype=torch.bfloat16, device="cuda")
+    empty = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    gt.gtattn_fwd_cache(st.cache(), tQ, empty, ints(st.lengths), ints(offsets([T, 0])), out, 2, T, 0, H, 0.1, gt.GTATTN_BF16)
+    assert (out == 0).all()
+    out.fill_(77)
+    gt.gtattn_fwd_cache(gt.Cache.empty(0, 2, D, 16), tQ, ints(st.table), ints(st.lengths), ints(offsets([T, 0])), out, 2, T,
+                        st.max_pages, H, 0.1, gt.GTATTN_BF16)
+    assert (out == 0).all()
+
+
 def test_attend_tail_of_a_page_is_not_read():
     # what lies behind a request's last token in its page is NaN in a Store: it changes nothing
     rng = np.random.default_rng(12)
