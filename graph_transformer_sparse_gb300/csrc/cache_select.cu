@@ -95,6 +95,10 @@ template <typename T, int NCH> struct Query {
         norm += __shfl_xor_sync(0xffffffffu, norm, 2);
     }
 };
+// Roundings that a term of the dot product goes through: the FMAs of its
+// chain, two sums of chains, two of lanes.
+constexpr int dot_depth(int D) { return 2 * ((D + 31) / 32) + 4; }
+
 // One lane's pieces of a page's mean.
 template <int NCH> struct Mean {
     uint4 w[NCH];
@@ -120,18 +124,19 @@ template <int NCH> struct Mean {
     }
     // the score, and the bits of the largest |mean| (all four lanes)
     template <typename T> __device__ __forceinline__ void score(const Query<T, NCH>& q, float& s, uint32_t& big) const {
-        s = 0.f;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};      // (short chains: dot_depth)
         big = 0;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                s = fmaf(q.q[i][2 * k], bf16lo(x[k]), s);
-                s = fmaf(q.q[i][2 * k + 1], bf16hi(x[k]), s);
+                part[k] = fmaf(q.q[i][2 * k], bf16lo(x[k]), part[k]);
+                part[k] = fmaf(q.q[i][2 * k + 1], bf16hi(x[k]), part[k]);
                 big = __vmaxu2(big, x[k] & 0x7fff7fffu);
             }
         }
+        s = (part[0] + part[1]) + (part[2] + part[3]);
         s += __shfl_xor_sync(0xffffffffu, s, 1);
         s += __shfl_xor_sync(0xffffffffu, s, 2);
         big = max(big & 0xffffu, big >> 16);
@@ -172,6 +177,7 @@ constexpr int kPickThreads = 256;    // of k_pick
 constexpr int kFusedThreads = 128;   // of k_select
 constexpr int kPickKeys = 8192;      // keys held in shared memory; k_pick reads those of rows of more pages again
 constexpr int kPickClose = 128;      // close pages ranked in shared memory
+constexpr int kPickBins = 256;       // of the scores' histogram
 
 __device__ __forceinline__ uint32_t key_of(float x) {        // rises with x; -0 as 0
     const uint32_t u = __float_as_uint(x + 0.f);
@@ -268,6 +274,27 @@ __device__ __forceinline__ double exact_score(const SelArgs& a, const SelItem& i
     return v != v ? -INFINITY : v;
 }
 
+// The same without the sums at hand: the few pages that are scored again need
+// no barrier then (what it reads has just been read: it is in L1 or L2).
+template <typename T>
+__device__ __forceinline__ double exact_score_alone(const SelArgs& a, const SelItem& it, int p, int lane) {
+    const int pid = __ldg(a.r.table + static_cast<int64_t>(it.s) * a.r.max_pages + p);
+    const T* Q = static_cast<const T*>(a.Q) + (static_cast<int64_t>(it.t) * a.H + it.g * a.G) * a.c.D;
+    double v = 0;
+    if (static_cast<unsigned>(pid) < static_cast<unsigned>(a.c.pages)) {
+        const __nv_bfloat16* m = a.c.kmean + (static_cast<int64_t>(pid) * a.c.Hkv + it.g) * a.c.D;
+        for (int d = lane; d < a.c.D; d += 32) {
+            double q = 0;
+#pragma unroll 4
+            for (int h = 0; h < a.G; ++h) q += load_elem(Q, h * a.c.D + d);
+            v = fma(q, static_cast<double>(__bfloat162float(m[d])), v);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v != v ? -INFINITY : v;
+}
+
 // Lists the k best of the row's `own` earlier pages (own > k > 0), by a block.
 // held: the fp32 scores' keys stand in keys[0 .. own), to be seen after a
 // barrier, else in score[].x.  bits: those of this thread's largest |mean|.
@@ -283,47 +310,104 @@ __device__ __forceinline__ void pick_pages(const SelArgs& a, const SelItem& it, 
     __shared__ unsigned long long s_least[WARPS];
     __shared__ int z_at[kPickClose];
     __shared__ double z_score[kPickClose];
-    __shared__ int z_n;
+    __shared__ int z_n, z_members;
+    __shared__ int s_bin[kPickBins];
+    __shared__ uint32_t z_key[kPickClose], s_kth;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int own = it.own, k = a.n_sel - 1;
     BlockSum<THREADS> sum{s_sums, 0};
     auto key = [&](int i) { return held ? keys[i] : key_of(score[i].x); };
     __syncthreads();
-    uint32_t any = 0, every = 0xffffffffu;
+    uint32_t highest = 0, lowest = 0xffffffffu;       // the largest and the least key
     for (int i = tid; i < own; i += THREADS) {
         const uint32_t x = key(i);
-        any |= x;
-        every &= x;
+        highest = max(highest, x);
+        lowest = min(lowest, x);
     }
+    for (int i = tid; i < kPickBins; i += THREADS) s_bin[i] = 0;
     bits = __reduce_max_sync(0xffffffffu, bits);
-    any = __reduce_or_sync(0xffffffffu, any);
-    every = __reduce_and_sync(0xffffffffu, every);
+    highest = __reduce_max_sync(0xffffffffu, highest);
+    lowest = __reduce_min_sync(0xffffffffu, lowest);
     if (lane == 0) {
         s_red[0][warp] = bits;
-        s_red[1][warp] = any;
-        s_red[2][warp] = every;
+        s_red[1][warp] = highest;
+        s_red[2][warp] = lowest;
     }
-    if (tid == 0) z_n = 0;
+    if (tid == 0) z_n = z_members = 0;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         bits = max(bits, s_red[0][w]);
-        any |= s_red[1][w];
-        every &= s_red[2][w];
+        highest = max(highest, s_red[1][w]);
+        lowest = min(lowest, s_red[2][w]);
     }
     const float big = __uint_as_float(bits);         // (a NaN's bits are above all)
-    // roundings of one score: G - 1 in the group's sum, D / 4 + 2 in the dot product, one each product
-    const float gamma = (a.G + a.c.D / 4 + 8) * 6.0e-8f * 1.01f;
+    // roundings of one score: G - 1 in the group's sum, and the dot product's (2^-24 each, and their products)
+    const float gamma = (a.G + dot_depth(a.c.D)) * 6.0e-8f * 1.01f;
     const float bound = 2.f * (gamma * norm * big) + 1e-36f;     // 2E; the last: products below fp32's range
     float lo = 0.f, hi = 0.f;
     const bool all = !(bound < 1e37f) || !(norm < 1e37f) || !(big < 1e37f) || !(norm * big < 1e37f);
     bool redo = all;
     int mid = 0, want = 0;               // pages between, and how many of them are in
     if (!all) {
-        const uint32_t differ = any ^ every;
-        const uint32_t top = differ ? 1u << (31 - __clz(differ)) : 0u;
-        const uint32_t common = top ? every & ~(2 * top - 1) : every;
-        const float kth = key_value(kth_largest<THREADS, uint32_t>(own, k, common, top, key, sum, s_red[0]));
+        // the k-th largest: by a histogram over the scores' range and the members of its bin, or, where
+        // too many share that, bit by bit
+        const float least = key_value(lowest), width = key_value(highest) - least;
+        const float to_bin = width > 0.f ? (kPickBins - 1) / width : 0.f;
+        auto bin_of = [&](float x) { return min(kPickBins - 1, static_cast<int>((x - least) * to_bin)); };
+        for (int i = tid; i < own; i += THREADS) atomicAdd(&s_bin[bin_of(key_value(key(i)))], 1);
+        __syncthreads();
+        int here = -1, above = 0;        // the bin that the k-th is in, the keys in higher ones
+        {
+            constexpr int PER = kPickBins / 32;
+            int cnt[PER], mine = 0;      // lane 0 has the highest bins
+#pragma unroll
+            for (int i = 0; i < PER; ++i) mine += cnt[i] = s_bin[kPickBins - 1 - (lane * PER + i)];
+            int x = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            const int at = __ffs(__ballot_sync(0xffffffffu, x >= k)) - 1;       // (the last lane has all: own > k)
+            int run = x - mine;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (here < 0 && run + cnt[i] >= k) {
+                    here = kPickBins - 1 - (lane * PER + i);
+                    above = run;
+                }
+                run += cnt[i];
+            }
+            here = __shfl_sync(0xffffffffu, here, at);
+            above = __shfl_sync(0xffffffffu, above, at);
+        }
+        uint32_t kth_key;
+        if (s_bin[here] <= kPickClose) {
+            const int members = s_bin[here];
+            for (int i = tid; i < own; i += THREADS) {
+                const uint32_t x = key(i);
+                if (bin_of(key_value(x)) == here) z_key[atomicAdd(&z_members, 1)] = x;
+            }
+            __syncthreads();
+            for (int y = tid; y < members; y += THREADS) {
+                const uint32_t x = z_key[y];
+                int more = 0, same = 0;
+                for (int z = 0; z < members; ++z) {
+                    more += z_key[z] > x;
+                    same += z_key[z] == x;
+                }
+                if (above + more < k && k <= above + more + same) s_kth = x;      // (equal keys write the same)
+            }
+            __syncthreads();
+            kth_key = s_kth;
+        } else {
+            const uint32_t low = key_of(least), differ = low ^ highest;       // (keys between two share their common top)
+            const uint32_t top = differ ? 1u << (31 - __clz(differ)) : 0u;
+            const uint32_t common = top ? low & ~(2 * top - 1) : low;
+            kth_key = kth_largest<THREADS, uint32_t>(own, k, common, top, key, sum, s_red[0]);
+        }
+        const float kth = key_value(kth_key);
         const float pad = bound + fabsf(kth) * 3e-7f;            // (and the rounding of these two)
         lo = kth - pad;
         hi = kth + pad;
@@ -344,10 +428,8 @@ __device__ __forceinline__ void pick_pages(const SelArgs& a, const SelItem& it, 
     // few pages between (the usual case): each scored by a warp in 64 bits and
     // ranked among them; its fp32 score then says in or out
     if (redo && !all && mid <= kPickClose) {
-        query_sums<T, THREADS>(a, it, qs);
-        __syncthreads();
         for (int z = warp; z < mid; z += WARPS) {
-            const double v = exact_score(a, it, qs, z_at[z], lane);
+            const double v = exact_score_alone<T>(a, it, z_at[z], lane);
             if (lane == 0) z_score[z] = v;
         }
         __syncthreads();
