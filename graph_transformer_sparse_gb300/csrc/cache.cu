@@ -284,9 +284,9 @@ k_append(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const in
 // exact in fp32, in any order).  Prompts take a warp per run, which looks at
 // `span` consecutive tokens for runs that begin there: with a block per run
 // its barriers and set-up were most of the 350 instructions a thread spent on
-// 16 elements (17 k fp32 tokens of 8 x 64: APPEND_PROMPT).  Batches too small
+// 16 elements (14 k fp32 tokens of 8 x 64: 26.4 us, now 22.4).  Batches too small
 // to fill the SMs with warps take a block per run, four warps on the page's
-// rows (128 single tokens of 8 x 128: 6.4 us, with a warp 10.6: the earlier
+// rows (128 single tokens of 8 x 128: 7.2 us, with a warp 10.6: the earlier
 // keys that the mean reads come one after another).
 // Bound by memory: the new rows are read once from DRAM (the second pass over
 // them hits L1), a page's earlier keys are read for its mean.

@@ -5,7 +5,9 @@
 // group's queries are added first, so a page costs one dot product of D.  Two
 // steps: k_scores forms every score in fp32 -- it reads the page means, which
 // is what bounds the call -- and k_pick, a block per (token, head), finds the
-// k-th largest and lists the pages.
+// k-th largest and lists the pages; k_select does both where its items alone
+// fill the GPU.  64 requests of 9-32 thousand tokens, 8 K/V heads of 128: 16.6
+// us in one launch (11 of them reading 43 MB of means), 31 in two.
 //
 // The choice has to be that of 64 bits.  An fp32 score is off by at most
 // E = gamma * |q|_1 * max|kmean| (standard bound of a sum of products), so a

@@ -15,7 +15,11 @@
 // are the parts that k_cache_join adds up.
 //
 // Bound by the softmax's instructions (per element two FMAs, a maximum, an
-// exp2, half a conversion and an addition against 4 D product operations).
+// exp2, half a conversion and an addition against 4 D product operations): 4
+// requests adding 2000 tokens to 8000, 32 heads over 8 of 64, take 460 us
+// (469 TFLOP/s; the tiles of cache_tile.cuh 937 us), 8000-token prompts of 16
+// heads over 8 of 128 401 us (861).  From 64 rows a request and K/V head on:
+// with 17 tokens of 4 heads both take 61 us, with 64 tokens 115 against 143.
 // Every wait for the tensor cores is bounded: a block whose wait runs out
 // records an error (gtattn_device_errors), waits for what it issued, frees its
 // tensor memory and ends.

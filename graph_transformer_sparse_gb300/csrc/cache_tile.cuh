@@ -111,11 +111,11 @@ int blocks_per_sm(const void* kernel, int threads, int smem) {
 //
 // Both products are formed transposed, keys (or features) along the 16 of the
 // instruction and rows along its 8: logits^T = K Q^T, out^T = V^T weights^T.
-// A token's few heads then fill the tile (with rows along the 16, half the
-// instructions and the registers went to rows that are not there: 206
-// registers and 656 instructions a step at D = 128 instead of what ptxas and
-// the counters show now, and two warps a scheduler, whose waits could not be
-// hidden).  The weights, keys by rows as they come out, become the second
+// A token's few heads then fill the tile.  (With rows along the 16, half the
+// registers and of the softmax's instructions went to rows that are not there:
+// 206 registers at D = 128 against 157, so two warps a scheduler against
+// three, whose waits could not be hidden: 121 us for the 64 requests below in
+// this kernel, against 103.)  The weights, keys by rows as they come out, become the second
 // product's operand by one 8 x 8 transposition each (movmatrix).
 //
 // A block's four warps take the tile's keys 32 at a time in turn, each with a
@@ -135,8 +135,10 @@ int blocks_per_sm(const void* kernel, int threads, int smem) {
 // of lc units each, lc such that all items together make about kTasksPerBlock
 // tasks for each resident block.  Blocks claim tasks from a counter: equal
 // shares handed out beforehand left the SMs busy between 161 and 228 thousand
-// cycles of 238 (they do not all get the same share of the memory), 120 us
-// for 64 requests of 500-8191 tokens.  Where the cuts lie depends on the
+// cycles of 238 (they do not all get the same share of the memory).  Bound by
+// memory: 64 requests of 500-8191 tokens, 32 heads over 8 of 128, 103 us in
+// this kernel (5.5 TB/s of 6.8), 113 with the plan and the join; one request of
+// 262150 tokens 57 and 69 us.  Where the cuts lie depends on the
 // sizes alone, and k_cache_join adds up an item's parts in order, so results
 // do not depend on who took what.
 constexpr int kTileWarps = 4;
@@ -189,7 +191,7 @@ struct TileWork {
 // resident blocks an SM the registers are cut for, and stages a warp's ring has
 template <int D, int NT> constexpr int tile_blocks() { return D * NT <= 64 ? 4 : D * NT <= 128 ? 3 : 2; }
 template <int D, int NT> constexpr int tile_stages() {      // (228 KB an SM; 3 KB a block for the rest)
-    const int n = (228 * 1024 / tile_blocks<D, NT>() - 3072) / (kTileWarps * 2 * kStep * (D + 16));
+    const int n = (228 * 1024 / tile_blocks<D, NT>() - 3 * 1024) / (kTileWarps * 2 * kStep * (D + 16));
     return n < 8 ? n : 8;
 }
 template <int D> constexpr int tile_row() { return D + 16; }
