@@ -435,7 +435,7 @@ def test_attend_selected(dtype, H, Hkv, D, page):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("H,Hkv,D", [(4, 4, 32), (8, 2, 64), (8, 1, 128), (4, 2, 48)])
+@pytest.mark.parametrize("H,Hkv,D", [(4, 4, 32), (8, 2, 64), (8, 1, 128), (4, 2, 48), (2, 1, 256), (3, 3, 7)])
 def test_attend_long_requests(dtype, H, Hkv, D):
     rng = np.random.default_rng(D)
     st = Store(rng, [7001, 3, 2600], Hkv, D, 32)
