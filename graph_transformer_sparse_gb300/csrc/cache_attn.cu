@@ -161,7 +161,10 @@ extern "C" gtattn_status gtattn_fwd_cache(const gtattn_cache* cache, const void*
         case 32: return cache_tile_32(a, dtype, rows, stream);
         case 64: return cache_tile_64(a, dtype, rows, stream);
         case 128: return cache_tile_128(a, dtype, rows, stream);
-        default: break;
+        default:
+            if (a.c.D % 16 == 0 && a.c.D < 64) return cache_tile_to_64(a, dtype, stream);
+            if (a.c.D % 16 == 0 && a.c.D < 128) return cache_tile_to_128(a, dtype, stream);
+            break;
     }
     const int64_t items = T * H;
     // shares: about eight blocks an SM, eight pages a block and share at least

@@ -22,6 +22,9 @@ struct CacheAttn {
 gtattn_status cache_tile_32(const CacheAttn& a, gtattn_dtype dtype, int64_t rows, cudaStream_t s);
 gtattn_status cache_tile_64(const CacheAttn& a, gtattn_dtype dtype, int64_t rows, cudaStream_t s);
 gtattn_status cache_tile_128(const CacheAttn& a, gtattn_dtype dtype, int64_t rows, cudaStream_t s);
+// The same for narrower heads, a multiple of 16 features, padded in shared memory.
+gtattn_status cache_tile_to_64(const CacheAttn& a, gtattn_dtype dtype, cudaStream_t s);
+gtattn_status cache_tile_to_128(const CacheAttn& a, gtattn_dtype dtype, cudaStream_t s);
 
 // The same for many rows, on tcgen05 (cache_tc.cu): whether it takes the
 // call, and the call.

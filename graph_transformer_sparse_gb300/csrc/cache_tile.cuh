@@ -481,7 +481,9 @@ struct Reach {
 };
 __device__ __forceinline__ int pt_first(const Task& t, int warp) { return t.j0 * kTileWarps + warp; }
 
-template <typename TI, typename TO, int D, int NT, bool SPLITQ, bool SPLITP>
+// PAD: heads of c.D < D features, a multiple of 16: rows of them in memory, of
+// D, zeros behind, in shared memory and registers.
+template <typename TI, typename TO, int D, int NT, bool SPLITQ, bool SPLITP, bool PAD = false>
 __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cache_attn_tile(CacheAttn a, TileWork wk) {
     constexpr int R = 8 * NT, RJ = R < 16 ? R : 16, NST = tile_stages<D, NT>(), ROW = tile_row<D>(), STAGE = 2 * kStep * ROW;
     constexpr int OROW = D + 4;     // row stride of a warp's output in the join, in floats
@@ -499,6 +501,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cac
     const int r = lane >> 2, cq = lane & 3;
     const CacheView& c = a.c;
     const int Hkv = c.Hkv, page = c.page;
+    const int width = PAD ? c.D : D;       // features of a head in memory
     uint8_t* ring = smem + warp * NST * STAGE;
     const uint32_t ring_u = smem_u32(ring);
     let_next_start();
@@ -608,10 +611,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cac
             const int pid = __shfl_sync(full, cur.pid[q], from);
             const int m = (cnt >> (8 * q)) & 0xff;
             const int off = ((pt.first + pk * kTileWarps) * kStep + 16 * q) & (page - 1);
-            const int64_t src = (((static_cast<int64_t>(pid) * Hkv + pt.g) << c.lp) + off) * D;
+            const int64_t src = (((static_cast<int64_t>(pid) * Hkv + pt.g) << c.lp) + off) * width;
             // 16 rows of D bytes, contiguous: lane i's 16 bytes are in row i / (D / 16) and every 512 / D rows on
             const uint32_t to = dst + dlane + 16 * q * ROW;
-            if (m == 16) {
+            if (!PAD && m == 16) {
                 const uint8_t* kp = c.k8 + src + lane * 16;
                 const uint8_t* vp = c.v8 + src + lane * 16;
 #pragma unroll
@@ -622,8 +625,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cac
             } else {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
-                    const bool ok = lane / (D / 16) + i * (512 / D) < m;
-                    const int64_t at = src + (ok ? lane * 16 + i * 512 : 0);
+                    const int row = lane / (D / 16) + i * (512 / D), col = lane % (D / 16) * 16;
+                    const bool ok = row < m && (!PAD || col < width);
+                    const int64_t at = src + (ok ? row * width + col : 0);
                     copy16_or_zero(to + i * (512 / D) * ROW, c.k8 + at, ok);
                     copy16_or_zero(to + i * (512 / D) * ROW + kStep * ROW, c.v8 + at, ok);
                 }
@@ -660,9 +664,14 @@ __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cac
             const bool valid = nt * 8 + r < it.rows;
             const int q = it.q0 + (valid ? nt * 8 + r : 0);
             const int tok = a.sel ? 0 : q / a.G, hd = it.g * a.G + (a.sel ? q : q % a.G);
-            const int64_t src = (static_cast<int64_t>(it.t0 + tok) * a.H + hd) * D + cq * (D / 4);
+            const int64_t src = (static_cast<int64_t>(it.t0 + tok) * a.H + hd) * width + cq * (D / 4);
             float x[D / 4];
-            load_part<TI, D / 4>(static_cast<const TI*>(a.Q) + src, a.q_vec != 0, x);
+            if constexpr (PAD) {
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) x[i] = cq * (D / 4) + i < width ? load_elem(static_cast<const TI*>(a.Q), src + i) : 0.f;
+            } else {
+                load_part<TI, D / 4>(static_cast<const TI*>(a.Q) + src, a.q_vec != 0, x);
+            }
             float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 4; ++i) {
@@ -920,8 +929,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, (tile_blocks<D, NT>())) k_cac
                 if (out_slot < 0) {
                     const int q = it.q0 + j0r + row;
                     const int tok = a.sel ? 0 : q / a.G, hd = it.g * a.G + (a.sel ? q : q % a.G);
-                    store_out<TO>(static_cast<TO*>(a.out), (static_cast<int64_t>(it.t0 + tok) * a.H + hd) * D + d, acc, sum,
-                                  a.o_vec != 0);
+                    if (!PAD || d < width)
+                        store_out<TO>(static_cast<TO*>(a.out), (static_cast<int64_t>(it.t0 + tok) * a.H + hd) * width + d, acc, sum,
+                                      a.o_vec != 0);
                 } else {
                     const int64_t at = static_cast<int64_t>(out_slot) * R + j0r + row;
                     *reinterpret_cast<float4*>(wk.part_o + at * D + d) = acc;
@@ -953,7 +963,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) k_cache_join(CacheAttn a, 
     auto out_at = [&](const Item& it, int row) {
         const int x = it.q0 + row;
         const int tok = a.sel ? 0 : x / a.G, hd = it.g * a.G + (a.sel ? x : x % a.G);
-        return (static_cast<int64_t>(it.t0 + tok) * a.H + hd) * D;
+        return (static_cast<int64_t>(it.t0 + tok) * a.H + hd) * a.c.D;      // (a.c.D < D: padded heads)
     };
     constexpr int GROUPS = R / kJoinWarps;
     for (unsigned long long j = blockIdx.x; j < static_cast<unsigned long long>(items) * GROUPS; j += gridDim.x) {
@@ -982,7 +992,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) k_cache_join(CacheAttn a, 
             const int64_t at = out_at(t.it, row);
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                store_elem(static_cast<TO*>(a.out), at + v * 32 + lane, sum == 0.f ? 0.f : acc[v] / sum);
+                if (v * 32 + lane < a.c.D)
+                    store_elem(static_cast<TO*>(a.out), at + v * 32 + lane, sum == 0.f ? 0.f : acc[v] / sum);
         }
     }
     if (!longer) return;
@@ -1020,7 +1031,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) k_cache_join(CacheAttn a, 
         if (lane == 0) s_sum[warp] = sum;
         __syncthreads();
         const int d = threadIdx.x;
-        if (d < D) {
+        if (d < a.c.D) {
             float o = 0.f, total = 0.f;
 #pragma unroll
             for (int w = 0; w < kJoinWarps; ++w) {
@@ -1097,6 +1108,16 @@ template <int D, int NT> gtattn_status launch_tile_n(const CacheAttn& a, gtattn_
     if (dtype == GTATTN_F32) return launch_tile<float, float, D, NT, true, true>(a, s);
     if (dtype == GTATTN_BF16) return launch_tile<B, B, D, NT, false, false>(a, s);
     return launch_tile<B, float, D, NT, false, true>(a, s);
+}
+// Heads of a.c.D < D features, 16 rows a tile.
+template <int D> gtattn_status launch_tile_padded(const CacheAttn& a, gtattn_dtype dtype, cudaStream_t s) {
+    using B = __nv_bfloat16;
+    constexpr int threads = kTileWarps * 32, smem = tile_smem<D, 2>();
+    if (dtype == GTATTN_F32)
+        return launch_planned<float, D, 16>(k_cache_attn_tile<float, float, D, 2, true, true, true>, threads, smem, kTasksPerBlock, a, s);
+    if (dtype == GTATTN_BF16)
+        return launch_planned<B, D, 16>(k_cache_attn_tile<B, B, D, 2, false, false, true>, threads, smem, kTasksPerBlock, a, s);
+    return launch_planned<float, D, 16>(k_cache_attn_tile<B, float, D, 2, false, true, true>, threads, smem, kTasksPerBlock, a, s);
 }
 // 8, 16 or 32 rows a tile, by the rows that a request brings per K/V head (32
 // not at D = 128 nor, with its queries in two parts, in fp32: registers).

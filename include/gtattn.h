@@ -573,10 +573,10 @@ gtattn_status gtattn_cache_select(const gtattn_cache* cache, const void* Q, cons
  * row's result reads only the tokens it may see (a NaN in a later token or
  * an unused place reaches no earlier row).  Queries are held to 2^-40 of
  * their row's largest; the softmax weights in 11 bits where out is bf16, in 21
- * or more where it is fp32.  D = 32, 64 and 128 run on the tensor cores
- * (tcgen05 from 64 rows a request and K/V head on, bf16 queries, D 64 or 128,
- * no sel), other widths on the CUDA cores; a bounded device wait that gives up
- * is reported by gtattn_device_errors.
+ * or more where it is fp32.  D up to 128 that is a multiple of 16 runs on the
+ * tensor cores (tcgen05 from 64 rows a request and K/V head on, bf16 queries,
+ * D 64 or 128, no sel), other widths on the CUDA cores; a bounded device wait
+ * that gives up is reported by gtattn_device_errors.
  * Errors: INVALID_ARG, UNSUPPORTED (T * H >= 2^31), NO_MEMORY, CUDA.
  */
 gtattn_status gtattn_fwd_cache(const gtattn_cache* cache, const void* Q, const int32_t* table, const int32_t* length,

@@ -397,7 +397,7 @@ def check_attend(st, Q, tQ, off, H, dtype, scale, sel=None, lengths=None):
 
 
 SHAPES = [(1, 1, 32, 16), (4, 4, 32, 16), (8, 8, 64, 32), (8, 2, 64, 16), (16, 2, 128, 64), (32, 4, 128, 32), (20, 1, 64, 64),
-          (3, 3, 128, 16), (40, 1, 32, 32), (6, 2, 1, 16), (4, 2, 80, 32), (4, 2, 256, 64), (5, 5, 33, 16)]
+          (3, 3, 128, 16), (40, 1, 32, 32), (6, 2, 1, 16), (4, 2, 80, 32), (4, 2, 256, 64), (5, 5, 33, 16), (6, 3, 16, 16), (4, 1, 48, 64), (8, 2, 112, 32)]
 
 
 @pytest.mark.parametrize("dtype", list(DT))
@@ -435,7 +435,7 @@ def test_attend_selected(dtype, H, Hkv, D, page):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("H,Hkv,D", [(4, 4, 32), (8, 2, 64), (8, 1, 128), (4, 2, 48), (2, 1, 256), (3, 3, 7)])
+@pytest.mark.parametrize("H,Hkv,D", [(4, 4, 32), (8, 2, 64), (8, 1, 128), (4, 2, 48), (4, 2, 96), (2, 1, 256), (3, 3, 7)])
 def test_attend_long_requests(dtype, H, Hkv, D):
     rng = np.random.default_rng(D)
     st = Store(rng, [7001, 3, 2600], Hkv, D, 32)
@@ -456,7 +456,7 @@ def test_attend_a_piece_of_a_prompt(dtype, H, Hkv, D, page):
     check_attend(st, Q, tQ, off, H, dtype, D ** -0.5)
 
 
-@pytest.mark.parametrize("D", [32, 64, 128, 40])
+@pytest.mark.parametrize("D", [32, 64, 128, 40, 96])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attend_nan_reaches_only_its_rows(D, dtype):
     # a NaN in key or value of a late token: rows before it do not see it, rows from it on do
@@ -473,7 +473,7 @@ def test_attend_nan_reaches_only_its_rows(D, dtype):
         assert seen[10:20].all() and not seen[:10].any() and not seen[20:].any()
 
 
-@pytest.mark.parametrize("D", [32, 64, 128, 40])
+@pytest.mark.parametrize("D", [32, 64, 128, 40, 96])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attend_extremes(D, dtype):
     # scales of pages far apart, large logits of either sign, equal keys, queries of very unlike sizes
@@ -539,7 +539,7 @@ def test_attend_many_rows_odd_values(D, dtype):
     check_attend(st, Q, tQ, off, H, dtype, -0.3, lengths=[120, -9])
 
 
-@pytest.mark.parametrize("D", [64, 40])
+@pytest.mark.parametrize("D", [64, 40, 48])
 def test_attend_bad_pages_and_lengths(D):
     rng = np.random.default_rng(11)
     H, Hkv, page = 4, 2, 16
