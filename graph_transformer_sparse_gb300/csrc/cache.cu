@@ -284,9 +284,9 @@ k_append(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const in
 // exact in fp32, in any order).  Prompts take a warp per run, which looks at
 // `span` consecutive tokens for runs that begin there: with a block per run
 // its barriers and set-up were most of the 350 instructions a thread spent on
-// 16 elements (14 k fp32 tokens of 8 x 64: 26.4 us, now 22.4).  Batches too small
+// 16 elements (14 k fp32 tokens of 8 x 64: 26.4 us, now 21.4).  Batches too small
 // to fill the SMs with warps take a block per run, four warps on the page's
-// rows (128 single tokens of 8 x 128: 7.2 us, with a warp 10.6: the earlier
+// rows (128 single tokens of 8 x 128: 7.0 us, with a warp 10.6: the earlier
 // keys that the mean reads come one after another).
 // Bound by memory: the new rows are read once from DRAM (the second pass over
 // them hits L1), a page's earlier keys are read for its mean.
@@ -341,7 +341,9 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
     __shared__ uint32_t red[WARPS];
     __shared__ float cols[WPR > 1 ? WARPS : 1][WPR > 1 ? kCacheMaxD : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int head = WPR > 1 ? blockIdx.y : blockIdx.y * WARPS + warp;            // K and V of each K/V head in turn
+    // K and V of each K/V head in turn; the heads of a token side by side in the grid (they share DRAM pages)
+    const unsigned heads = WPR > 1 ? 2 * c.Hkv : (2 * c.Hkv + WARPS - 1) / WARPS;
+    const int head = WPR > 1 ? blockIdx.x % heads : (blockIdx.x % heads) * WARPS + warp;
     if (head >= 2 * c.Hkv) return;
     auto run_max = [&](uint32_t v) {     // over the run's warps
         v = __reduce_max_sync(full, v);
@@ -358,7 +360,7 @@ k_append8(CacheView c, const T* __restrict__ K, const T* __restrict__ V, const i
     const bool is_v = head & 1;
     const int D = c.D, HD = c.Hkv * D, W = 1 << l8;
     const unsigned total = static_cast<unsigned>(c.pages) * c.page;
-    const int first = static_cast<int>(min(static_cast<long long>(blockIdx.x) * span, 0x7fffffffll));
+    const int first = static_cast<int>(min(static_cast<long long>(blockIdx.x / heads) * span, 0x7fffffffll));
     const int cc = lane & (W - 1), rows = (32 * WPR) >> l8;                       // this lane's columns, the row step
     const int rr = (WPR > 1 ? warp * 32 + lane : lane) >> l8;                     // and its first row
     const bool mean = !is_v && c.kmean;
@@ -526,7 +528,8 @@ extern "C" gtattn_status gtattn_cache_append(const gtattn_cache* cache, const vo
         constexpr int WARPS = kAppendThreads / 32;
         const bool block = span == 1;
         const auto go = [&](auto* one, auto* all, auto* Kp, auto* Vp) {
-            const dim3 grid((unsigned)((T + span - 1) / span), (unsigned)(block ? 2 * c.Hkv : (2 * c.Hkv + WARPS - 1) / WARPS));
+            const int64_t heads = block ? 2 * c.Hkv : (2 * c.Hkv + WARPS - 1) / WARPS;
+            const dim3 grid((unsigned)((T + span - 1) / span * heads));     // (below 2^31: so many rows fill no GPU)
             return launch_after(block ? all : one, grid, kAppendThreads, 0, stream, c, Kp, Vp, slots, (int)T, span, l8);
         };
         using B = __nv_bfloat16;
