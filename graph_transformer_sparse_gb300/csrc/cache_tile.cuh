@@ -4,9 +4,7 @@
 #pragma once
 
 #include <algorithm>
-#include <map>
 #include <mutex>
-#include <utility>
 
 #include "cache_attn.cuh"
 
@@ -83,20 +81,26 @@ __device__ void hide_nan(uint8_t* vt, const int (&rpos)[NT][2], int key0, int r,
 }
 
 // Blocks of a kernel that fit an SM at once, its dynamic shared memory
-// allowed first (0: error); asked once per kernel and device.
+// allowed first (0: error); asked once per kernel and device (and again where
+// the table is full: nothing here allocates or throws).
 int blocks_per_sm(const void* kernel, int threads, int smem) {
+    struct Known {
+        const void* kernel;
+        int dev, n;
+    };
     static std::mutex mu;
-    static std::map<std::pair<const void*, int>, int> known;
+    static Known known[64];
+    static int count = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     std::lock_guard<std::mutex> g(mu);
-    auto at = known.find({kernel, dev});
-    if (at != known.end()) return at->second;
+    for (int i = 0; i < count; ++i)
+        if (known[i].kernel == kernel && known[i].dev == dev) return known[i].n;
     int n = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess)
         return 0;
-    known[{kernel, dev}] = n;
+    if (count < 64) known[count++] = Known{kernel, dev, n};
     return n;
 }
 
